@@ -221,7 +221,7 @@ def prepare(case, seed):
         if block and case["shared"]:
             for a, b in zip(src, dst):
                 st["table"][b, : lens[a] // block] = st["table"][a, : lens[a] // block]
-        st["src"], st["dst"] = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (src, dst))
+        st["src"], st["dst"] = src, dst  # the scheduler's lists
     else:
         lens_now = lens
     st["lens"] = torch.tensor(lens_now, dtype=torch.int32, device="cuda")
@@ -360,7 +360,8 @@ def _plain_commit(st):
 
 
 def _plain_fork(st):
-    src, dst, lens, table = st["src"].long(), st["dst"].long(), st["lens"], st["table"]
+    lens, table = st["lens"], st["table"]
+    src, dst = torch.tensor(st["src"], device=lens.device), torch.tensor(st["dst"], device=lens.device)
     at = torch.arange(st["cap"], device=src.device)
     moves = at < lens.long()[src][:, None]                 # [children, cap]
     if table is not None:
@@ -472,7 +473,7 @@ def exact(case, seed):
                 for j, node in enumerate(path):
                     _put_row(x, table, s, n + j, rows[:, :, n + node])
     else:
-        for a, b in zip(st["src"].tolist(), st["dst"].tolist()):
+        for a, b in zip(st["src"], st["dst"]):
             for x in (k, v):
                 n = lens[a]
                 if table is None:
