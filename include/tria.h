@@ -493,6 +493,152 @@ tria_status tria_decode_attention(const tria_stats *stats, const tria_cache_view
                                   float *lse, float *logits, void *workspace,
                                   size_t workspace_bytes, tria_stream_t stream);
 
+/*
+ * tria_prompt_attention - attention over whole prompts: what fills the cache
+ * before the first decode step.  n_seq sequences lie packed one after another
+ * in q, k and v: sequence s is rows [seq_starts[s], seq_starts[s + 1]).  For
+ * row i and query head qh of KV head h = qh / G, over the rows j <= i of the
+ * same sequence (causal):
+ *   z_ij = scale * (q_i . k_j),  out_i = sum_j softmax(z_i)_j v_j,
+ *   lse_i = log sum_j exp(z_ij)
+ *   desc    n_q_heads, n_kv_heads and head_dim are read
+ *   q, k, v device bf16; element (row, head, dim) of x at
+ *           x[row * x_stride_token + head * x_stride_head + dim], so the three
+ *           may be slices of one fused projection.  16-byte aligned, strides
+ *           multiples of 8 elements, x_stride_token > 0, x_stride_head > 0.
+ *   n_tokens    rows that q, k, v, out and lse have; 0 is a call without work
+ *   seq_starts  device int32 [n_seq + 1], non-decreasing in [0, n_tokens].  A
+ *               sequence with a bad pair of starts sets status bit 0 and is
+ *               skipped; empty sequences are allowed.
+ *   scale   softmax scale, finite and > 0
+ *   out     device bf16 [n_tokens][n_q_heads][128] (16-byte aligned,
+ *           contiguous): sums in fp32, rounded once.  May not overlap q, k, v.
+ *   lse     optional device fp32 [n_tokens][n_q_heads] (natural log)
+ * Rows of no sequence (before seq_starts[0], behind seq_starts[n_seq]) are
+ * left as they are in out and lse, and what q, k, v hold there has no effect.
+ * A row depends on the rows j <= i of its sequence alone: infinities and NaN
+ * in later rows or in other sequences do not reach it.
+ * Workspace: tria_prompt_workspace_size bytes (256-byte aligned); its first
+ * 256 bytes hold the status flags read by tria_read_device_status.  Calls
+ * that may overlap need separate workspaces.
+ * The result does not depend on how the work is spread: equal inputs give
+ * equal bits.  Errors: INVALID_ARG, UNSUPPORTED (head_dim != 128, G not a
+ * power of two up to 16, strides a tensor map cannot express), WORKSPACE, CUDA.
+ */
+tria_status tria_prompt_workspace_size(const tria_model_desc *desc, int n_seq, size_t *bytes);
+tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q,
+                                  int64_t q_stride_token, int64_t q_stride_head, const void *k,
+                                  int64_t k_stride_token, int64_t k_stride_head, const void *v,
+                                  int64_t v_stride_token, int64_t v_stride_head, int64_t n_tokens,
+                                  const int32_t *seq_starts, int n_seq, float scale, void *out,
+                                  float *lse, void *workspace, size_t workspace_bytes,
+                                  tria_stream_t stream);
+
+/*
+ * tria_tree_attention - attention of drafted tokens over the cached rows of
+ * one layer: the verification step of speculative decoding, on the cache that
+ * the pass pruned.  Sequence s has N committed rows (its entry of seq_lens or
+ * layer_seq_lens) and T_s = draft_starts[s + 1] - draft_starts[s] drafted
+ * tokens, whose K and V rows the caller has written to the slots N .. N+T_s-1
+ * behind them.  Drafted token i of sequence s is row draft_starts[s] + i of q,
+ * mask, out and lse; it attends to every committed row and to the drafted rows
+ * that its mask names:
+ *   z_ij = scale * (q_i . k_j),  out_i = sum_j softmax(z_i)_j v_j,
+ *   lse_i = log sum_j exp(z_ij)
+ *   q       device bf16, element (token, head, dim) at q[token * q_stride_token
+ *           + head * q_stride_head + dim]; 16-byte aligned, strides positive
+ *           multiples of 8 elements; post-RoPE, like the cached keys
+ *   n_tokens      rows of q, mask, out and lse; 0 is a call without work
+ *   draft_starts  device int32 [n_seq + 1], non-decreasing in [0, n_tokens]
+ *   max_draft     host: upper bound of every T_s, 1 .. max_seq_len
+ *   mask    device uint32 [n_tokens][mask_words] with mask_words >=
+ *           ceil(max_draft / 32): bit b of word w of a token's row allows
+ *           drafted row 32 w + b of its sequence (a tree: the token's
+ *           ancestors and the token itself; any set is allowed; bits from T_s
+ *           on have no effect).  NULL: a chain, the drafted rows <= i
+ *           (mask_words is not read).
+ *   scale   softmax scale, finite and > 0
+ *   out     device bf16 [n_tokens][n_q_heads][128] (16-byte aligned, contiguous)
+ *   lse     optional device fp32 [n_tokens][n_q_heads] (natural log)
+ * A token that may attend to nothing (N = 0, mask 0) gets out = 0 and
+ * lse = -inf.  Rows outside a token's set do not reach its output, whatever
+ * they hold.  A sequence with a bad pair of starts, T_s > max_draft, N outside
+ * [0, max_seq_len] or N + T_s > max_seq_len sets status bit 0 and is skipped
+ * (its rows are left as they are).  Paged block ids outside [0, num_blocks)
+ * read as zero rows.  The cache is only read.  query_pos is not used.
+ * T_s = 1 is a decode step whose own row counts as drafted.
+ * Workspace: tria_tree_workspace_size bytes (256-byte aligned); status flags
+ * as in tria_prompt_attention.  Calls that may overlap need separate
+ * workspaces.  Equal inputs give equal bits.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+tria_status tria_tree_workspace_size(const tria_stats *stats, const tria_cache_view *cache,
+                                     int max_draft, size_t *bytes);
+tria_status tria_tree_attention(const tria_stats *stats, const tria_cache_view *cache, int layer,
+                                const void *q, int64_t q_stride_token, int64_t q_stride_head,
+                                int64_t n_tokens, const int32_t *draft_starts, int max_draft,
+                                const uint32_t *mask, int mask_words, float scale, void *out,
+                                float *lse, void *workspace, size_t workspace_bytes,
+                                tria_stream_t stream);
+
+/*
+ * tria_tree_commit - keep the accepted path of the drafted tokens: in every
+ * layer of [layer0, layer1) and KV head, the K and V rows (and positions, if
+ * the view has them) of drafted node accepted[s][j] move to slot N + j, in
+ * place, and the length grows by n_accepted[s].
+ *   accepted    device int32 [n_seq][max_accept]: the first n_accepted[s]
+ *               entries of a row are node numbers (slot N + node), strictly
+ *               ascending, as a path from the root is when parents come
+ *               before their children; later entries are not read
+ *   n_accepted  device int32 [n_seq], 0 .. max_accept
+ * Lengths: without layer_seq_lens, seq_lens[s] grows when layer1 == n_layers
+ * (call the layers in one go, or the last one last); with it, the entries of
+ * the covered layers grow.  A (sequence, layer) with N outside [0,
+ * max_seq_len], a bad n_accepted, or a path that is not strictly ascending
+ * inside [0, max_seq_len - N) sets status bit 0 and is left unchanged.  A move
+ * from or to a paged block id outside [0, num_blocks) does not happen and sets
+ * status bit 0.  Rows behind the new length keep what they held or what the
+ * drafted rows left there.  query_pos is not used.
+ * Workspace: tria_commit_workspace_size bytes (256-byte aligned), all zero
+ * before its first use (it holds arrival counts that every call leaves at
+ * zero); its first 256 bytes hold the status flags.  Calls that may overlap
+ * need separate workspaces.  Errors: INVALID_ARG, WORKSPACE, CUDA.
+ */
+tria_status tria_commit_workspace_size(const tria_stats *stats, const tria_cache_view *cache,
+                                       size_t *bytes);
+tria_status tria_tree_commit(const tria_stats *stats, const tria_cache_view *cache,
+                             const int32_t *accepted, const int32_t *n_accepted, int max_accept,
+                             int layer0, int layer1, void *workspace, size_t workspace_bytes,
+                             tria_stream_t stream);
+
+/*
+ * tria_fork_sequences - copy sequences inside the cache: the N rows (K, V and
+ * positions) of sequence src[i] become rows 0 .. N-1 of sequence dst[i] in the
+ * layers [layer0, layer1), and dst[i] gets src[i]'s length.  Paged layout: the
+ * caller has filled dst[i]'s row of the block table; where both rows name the
+ * same block, that block is shared and not copied (positions are copied).  So
+ * sharing every whole block copies only the one still being filled, and a
+ * table row of new blocks makes a private copy.  tria_compact and
+ * tria_compress_pass move rows in place: a sequence that shares blocks gets a
+ * private copy before a pass over it.
+ *   src, dst  host int32 [n_fork], sequence indices in [0, n_seq).  One source
+ *             may have many destinations; a destination occurs once and is no
+ *             source.  n_fork 0 is a call without work.
+ * Lengths: without layer_seq_lens, seq_lens[dst] is written when layer1 ==
+ * n_layers; with it, the entries of the covered layers.  A source whose N lies
+ * outside [0, max_seq_len] sets status bit 0 and is skipped.  A block id
+ * outside [0, num_blocks) in either row sets status bit 0 and its rows are not
+ * copied.  Rows of dst from N on are left as they are.  query_pos is not used.
+ * Workspace: tria_fork_workspace_size bytes (256-byte aligned): the status
+ * flags.  Errors: INVALID_ARG, WORKSPACE, CUDA.
+ */
+tria_status tria_fork_workspace_size(const tria_stats *stats, const tria_cache_view *cache,
+                                     size_t *bytes);
+tria_status tria_fork_sequences(const tria_stats *stats, const tria_cache_view *cache,
+                                const int32_t *src, const int32_t *dst, int n_fork, int layer0,
+                                int layer1, void *workspace, size_t workspace_bytes,
+                                tria_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

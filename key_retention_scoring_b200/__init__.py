@@ -32,7 +32,10 @@ EXPORTS = ["tria_status_string", "tria_version", "tria_load_stats", "tria_free_s
            "tria_compress_pass", "tria_read_device_status", "tria_set_pass_events",
            "tria_compress_pass_static", "tria_calib_accumulate", "tria_calib_finalize",
            "tria_layer_budgets", "tria_decode_workspace_size", "tria_decode_attention",
-           "tria_write_stats_file", "tria_read_stats_file"]
+           "tria_write_stats_file", "tria_read_stats_file", "tria_prompt_workspace_size",
+           "tria_prompt_attention", "tria_tree_workspace_size", "tria_tree_attention",
+           "tria_commit_workspace_size", "tria_tree_commit", "tria_fork_workspace_size",
+           "tria_fork_sequences"]
 STATIC_SCRATCH_BYTES = 32 * 1024 * 1024   # TRIA_STATIC_SCRATCH_BYTES
 
 
@@ -119,6 +122,19 @@ def lib() -> ctypes.CDLL:
     L.tria_read_stats_file.argtypes = [ctypes.c_char_p, ctypes.POINTER(ModelDesc),
                                        ctypes.POINTER(_I), ctypes.POINTER(_I), _VP, _VP, _VP, _VP,
                                        _VP]
+    i64, size = ctypes.c_int64, ctypes.c_size_t
+    view = ctypes.POINTER(CacheView)
+    L.tria_prompt_workspace_size.argtypes = [ctypes.POINTER(ModelDesc), _I, ctypes.POINTER(size)]
+    L.tria_prompt_attention.argtypes = [ctypes.POINTER(ModelDesc), _VP, i64, i64, _VP, i64, i64, _VP,
+                                        i64, i64, i64, _VP, _I, ctypes.c_float, _VP, _VP, _VP, size,
+                                        _VP]
+    L.tria_tree_workspace_size.argtypes = [_VP, view, _I, ctypes.POINTER(size)]
+    L.tria_tree_attention.argtypes = [_VP, view, _I, _VP, i64, i64, i64, _VP, _I, _VP, _I,
+                                      ctypes.c_float, _VP, _VP, _VP, size, _VP]
+    L.tria_commit_workspace_size.argtypes = [_VP, view, ctypes.POINTER(size)]
+    L.tria_tree_commit.argtypes = [_VP, view, _VP, _VP, _I, _I, _I, _VP, size, _VP]
+    L.tria_fork_workspace_size.argtypes = [_VP, view, ctypes.POINTER(size)]
+    L.tria_fork_sequences.argtypes = [_VP, view, _VP, _VP, _I, _I, _I, _VP, size, _VP]
     for name in EXPORTS:
         if name not in ("tria_status_string", "tria_version"):
             getattr(L, name).restype = _I
@@ -400,6 +416,141 @@ def tria_decode_attention(stats, cache, layer, q, scale, out, workspace, lse=Non
                                        _ptr(workspace),
                                        workspace.numel() * workspace.element_size(),
                                        _stream(stream)), "tria_decode_attention")
+
+
+def _on_device(where, **tensors):
+    """The serving operators take plain pointers: each tensor must lie on the
+    current device, in the type and layout that the kernels read."""
+    import torch
+
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for name, (t, dtypes, dim, contiguous) in tensors.items():
+        if t is None:
+            continue
+        if t.get_device() != dev or dev < 0:
+            raise TriaError(1, f"{where}: {name} must be on the current CUDA device")
+        if t.dtype not in dtypes or t.dim() != dim:
+            raise TriaError(1, f"{where}: {name} must have {dim} dimensions and type {dtypes[0]}")
+        if contiguous and not t.is_contiguous():
+            raise TriaError(1, f"{where}: {name} must be contiguous")
+
+
+def _row_strides(t):
+    """(token, head) strides of [tokens, heads, 128]; a dimension of one entry
+    never advances, so any stride stands for it."""
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise TriaError(1, "rows must have unit stride inside a head")
+    return (st if t.shape[0] > 1 else max(st, sh * t.shape[1], 128),
+            sh if t.shape[1] > 1 else 128)
+
+
+def tria_prompt_workspace_size(desc: ModelDesc, n_seq: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().tria_prompt_workspace_size(ctypes.byref(desc), int(n_seq), ctypes.byref(out)),
+           "tria_prompt_workspace_size")
+    return out.value
+
+
+def tria_prompt_attention(desc, q, k, v, seq_starts, scale, out, workspace, lse=None, stream=None):
+    """Causal attention over packed prompts: q bf16 [tokens, n_q_heads, 128],
+    k and v bf16 [tokens, n_kv_heads, 128] (any token and head strides that are
+    multiples of 8, e.g. slices of one fused projection), seq_starts int32
+    [n_seq + 1]; out bf16 [tokens, n_q_heads, 128], lse optional fp32 [tokens,
+    n_q_heads]."""
+    import torch
+
+    bf, where = (torch.bfloat16,), "tria_prompt_attention"
+    _on_device(where, q=(q, bf, 3, False), k=(k, bf, 3, False), v=(v, bf, 3, False),
+               seq_starts=(seq_starts, (torch.int32,), 1, True), out=(out, bf, 3, True),
+               lse=(lse, (torch.float32,), 2, True), workspace=(workspace, (torch.uint8,), 1, True))
+    n, hq, hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
+    if (q.shape != (n, hq, 128) or k.shape != (n, hkv, 128) or v.shape != k.shape or out.shape != q.shape
+            or seq_starts.shape[0] < 2 or (lse is not None and lse.shape != (n, hq))):
+        raise TriaError(1, f"{where}: shapes")
+    _check(lib().tria_prompt_attention(
+        ctypes.byref(desc), q.data_ptr(), *_row_strides(q), k.data_ptr(), *_row_strides(k),
+        v.data_ptr(), *_row_strides(v), n, seq_starts.data_ptr(), seq_starts.shape[0] - 1,
+        scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        where)
+
+
+def tria_tree_workspace_size(stats, cache, max_draft) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().tria_tree_workspace_size(stats.handle, ctypes.byref(cache.view), int(max_draft),
+                                          ctypes.byref(out)), "tria_tree_workspace_size")
+    return out.value
+
+
+def tria_tree_attention(stats, cache, layer, q, draft_starts, max_draft, scale, out, workspace,
+                        mask=None, lse=None, stream=None):
+    """Attention of drafted tokens over the committed rows of layer `layer` and
+    the drafted rows behind them: q bf16 [tokens, n_q_heads, 128], draft_starts
+    int32 [n_seq + 1], mask int32 [tokens, words] (bit b of word w allows
+    drafted row 32 w + b; None: a chain); out bf16 [tokens, n_q_heads, 128],
+    lse optional fp32 [tokens, n_q_heads]."""
+    import torch
+
+    bf, where = (torch.bfloat16,), "tria_tree_attention"
+    words = (torch.int32, torch.uint32)
+    _on_device(where, q=(q, bf, 3, False), draft_starts=(draft_starts, (torch.int32,), 1, True),
+               out=(out, bf, 3, True), mask=(mask, words, 2, True),
+               lse=(lse, (torch.float32,), 2, True), workspace=(workspace, (torch.uint8,), 1, True))
+    n, hq = q.shape[0], stats.desc.n_q_heads
+    if (q.shape != (n, hq, 128) or out.shape != q.shape or draft_starts.shape[0] != cache.view.n_seq + 1
+            or (mask is not None and mask.shape[0] != n) or (lse is not None and lse.shape != (n, hq))):
+        raise TriaError(1, f"{where}: shapes")
+    _check(lib().tria_tree_attention(
+        stats.handle, ctypes.byref(cache.view), layer, q.data_ptr(), *_row_strides(q), n,
+        draft_starts.data_ptr(), max_draft, _ptr(mask), 0 if mask is None else mask.shape[1], scale,
+        out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+
+
+def tria_commit_workspace_size(stats, cache) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().tria_commit_workspace_size(stats.handle, ctypes.byref(cache.view),
+                                            ctypes.byref(out)), "tria_commit_workspace_size")
+    return out.value
+
+
+def tria_tree_commit(stats, cache, accepted, n_accepted, layer0, layer1, workspace, stream=None):
+    """Move the rows of accepted drafted nodes (accepted int32 [n_seq,
+    max_accept], ascending; n_accepted int32 [n_seq]) behind the committed rows
+    of layers [layer0, layer1) and grow the lengths."""
+    import torch
+
+    i32, where = (torch.int32,), "tria_tree_commit"
+    _on_device(where, accepted=(accepted, i32, 2, True), n_accepted=(n_accepted, i32, 1, True),
+               workspace=(workspace, (torch.uint8,), 1, True))
+    n = cache.view.n_seq
+    if accepted.shape[0] != n or n_accepted.shape[0] != n:
+        raise TriaError(1, f"{where}: shapes")
+    _check(lib().tria_tree_commit(stats.handle, ctypes.byref(cache.view), accepted.data_ptr(),
+                                  n_accepted.data_ptr(), accepted.shape[1], layer0, layer1,
+                                  workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+
+
+def tria_fork_workspace_size(stats, cache) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().tria_fork_workspace_size(stats.handle, ctypes.byref(cache.view),
+                                          ctypes.byref(out)), "tria_fork_workspace_size")
+    return out.value
+
+
+def tria_fork_sequences(stats, cache, src, dst, layer0, layer1, workspace, stream=None):
+    """Copy sequence src[i] to sequence dst[i] (host sequences of indices) in
+    layers [layer0, layer1): rows, positions and length; paged blocks that both
+    rows of the block table name are shared."""
+    import torch
+
+    where = "tria_fork_sequences"
+    _on_device(where, workspace=(workspace, (torch.uint8,), 1, True))
+    if len(src) != len(dst):
+        raise TriaError(1, f"{where}: src and dst must have the same length")
+    a, b = (np.ascontiguousarray(x, dtype=np.int32) for x in (src, dst))
+    _check(lib().tria_fork_sequences(stats.handle, ctypes.byref(cache.view), a.ctypes.data,
+                                     b.ctypes.data, len(a), layer0, layer1, workspace.data_ptr(),
+                                     workspace.numel(), _stream(stream)), where)
 
 
 def tria_read_device_status(workspace, stream=None) -> int:

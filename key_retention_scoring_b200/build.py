@@ -13,7 +13,8 @@ LIB = os.path.join(PKG, "libtria.so")
 SOURCES = ["tria_api.cu", "tria_kernels.cu", "tria_score_tc.cu", "tria_score_max.cu",
            "tria_score_grouped.cu", "tria_tail.cu",
            "tria_compact.cu",
-           "tria_calib.cu", "tria_static.cu", "tria_decode.cu", "tria_stats_io.cu"]
+           "tria_calib.cu", "tria_static.cu", "tria_decode.cu", "tria_stats_io.cu",
+           "tria_attend.cu", "tria_rows.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -35,7 +36,7 @@ def _stale() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "--threads", "0", "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-cudart", "static", "-I", INCLUDE, "-o", LIB + ".tmp"]
     if verbose:
         cmd += ["-Xptxas", "-v"]

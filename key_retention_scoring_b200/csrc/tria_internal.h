@@ -211,4 +211,44 @@ __host__ __device__ __forceinline__ bool compresses(const Geom &g, int n, int lr
   return len_valid(g, n) && n - g.lbudget[lrel] >= g.trigger;
 }
 
+// ---------------------------------------------------------------------------
+// Serving operators (tria_attend.cu, tria_rows.cu)
+// ---------------------------------------------------------------------------
+// A checked cache view for kernels that address rows themselves.
+struct RowsView {
+  int layout, block_size, max_blocks;
+  int n_seq, n_layers, hkv, max_seq_len;
+  int64_t s_seq, s_head, s_tok, s_blk, num_blocks;
+  const int32_t *block_table;
+  int32_t *lens;       // N of (s, layer) = lens[s * lens_s + layer * lens_l]
+  int64_t lens_s;
+  int lens_l;          // 1: a length per (sequence, layer), 0: one per sequence
+  int32_t *positions;
+};
+
+// Host checks of a view that the serving operators share (rows, strides,
+// table, lengths; K and V bases of layers [layer0, layer1)).
+tria_status make_rows_view(const tria_stats *stats, const tria_cache_view *cache, int layer0,
+                           int layer1, tria_model_desc *desc, RowsView *view);
+tria_status check_header_workspace(void *ws, size_t have, size_t need);
+
+constexpr size_t kHeaderBytes = 256;  // workspace header; status flags at byte 4
+
+// N of (s, layer), or -1 when it lies outside [0, max_seq_len]
+__host__ __device__ __forceinline__ int view_len(const RowsView &v, int s, int layer) {
+  const int n = v.lens[(int64_t)s * v.lens_s + (int64_t)layer * v.lens_l];
+  return (n >= 0 && n <= v.max_seq_len) ? n : -1;
+}
+
+// Element offset of slot t of (s, h); false for a block id outside the pool.
+__host__ __device__ __forceinline__ bool view_row(const RowsView &v, int s, int h, int t, int64_t *off) {
+  if (v.layout == TRIA_LAYOUT_CONTIGUOUS) {
+    *off = (int64_t)s * v.s_seq + (int64_t)h * v.s_head + (int64_t)t * v.s_tok;
+    return true;
+  }
+  const int blk = v.block_table[(int64_t)s * v.max_blocks + t / v.block_size];
+  *off = (int64_t)blk * v.s_blk + (int64_t)(t % v.block_size) * v.s_tok + (int64_t)h * v.s_head;
+  return blk >= 0 && blk < v.num_blocks;
+}
+
 }  // namespace tria

@@ -1,0 +1,399 @@
+// Moving cached rows: the accepted path of drafted tokens (tria_tree_commit)
+// and copies of whole sequences (tria_fork_sequences).  Both move K and V rows
+// of 256 bytes (and int32 positions) byte for byte, so what bounds them is HBM
+// (or, for a few rows, the latency of the chain length -> path -> block table
+// -> row -> store).
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "tria_device.cuh"
+
+namespace tria {
+
+tria_status make_rows_view(const tria_stats *stats, const tria_cache_view *c, int layer0, int layer1,
+                           tria_model_desc *desc, RowsView *view) {
+  if (stats == nullptr || c == nullptr) return TRIA_ERR_INVALID_ARG;
+  const tria_status st = tria_stats_desc(stats, desc);
+  if (st != TRIA_OK) return st;
+  if (layer0 < 0 || layer1 <= layer0 || layer1 > desc->n_layers) return TRIA_ERR_INVALID_ARG;
+  if (c->n_seq < 1 || c->n_seq > TRIA_MAX_SEQS || c->max_seq_len < 1) return TRIA_ERR_INVALID_ARG;
+  if (c->layout != TRIA_LAYOUT_CONTIGUOUS && c->layout != TRIA_LAYOUT_PAGED) return TRIA_ERR_INVALID_ARG;
+  if (c->k_layers == nullptr || c->v_layers == nullptr) return TRIA_ERR_INVALID_ARG;
+  if (c->layer_seq_lens == nullptr && c->seq_lens == nullptr) return TRIA_ERR_INVALID_ARG;
+  for (int l = layer0; l < layer1; ++l)
+    for (const void *p : {c->k_layers[l], c->v_layers[l]})
+      if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u)) return TRIA_ERR_INVALID_ARG;
+  if (c->stride_head < 0 || c->stride_token <= 0 || c->stride_seq < 0 || c->stride_block < 0 ||
+      (c->stride_head % 8) || (c->stride_token % 8) || (c->stride_seq % 8) || (c->stride_block % 8))
+    return TRIA_ERR_INVALID_ARG;
+  if (c->positions != nullptr && (reinterpret_cast<uintptr_t>(c->positions) & 3u)) return TRIA_ERR_INVALID_ARG;
+  const bool paged = c->layout == TRIA_LAYOUT_PAGED;
+  if (paged) {
+    const int bs = c->block_size;
+    if (c->block_table == nullptr || c->max_blocks_per_seq < 1 || c->num_blocks < 1 ||
+        !(bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs == 128) ||
+        (int64_t)c->max_blocks_per_seq * bs < c->max_seq_len)
+      return TRIA_ERR_INVALID_ARG;
+  }
+  RowsView v{};
+  v.layout = c->layout;
+  v.block_size = paged ? c->block_size : 1;
+  v.max_blocks = paged ? c->max_blocks_per_seq : 0;
+  v.n_seq = c->n_seq;
+  v.n_layers = desc->n_layers;
+  v.hkv = desc->n_kv_heads;
+  v.max_seq_len = c->max_seq_len;
+  v.s_seq = c->stride_seq;
+  v.s_head = c->stride_head;
+  v.s_tok = c->stride_token;
+  v.s_blk = c->stride_block;
+  v.num_blocks = paged ? c->num_blocks : 0;
+  v.block_table = c->block_table;
+  const bool per_layer = c->layer_seq_lens != nullptr;
+  v.lens = per_layer ? c->layer_seq_lens : c->seq_lens;
+  v.lens_s = per_layer ? desc->n_layers : 1;
+  v.lens_l = per_layer ? 1 : 0;
+  v.positions = c->positions;
+  *view = v;
+  return TRIA_OK;
+}
+
+tria_status check_header_workspace(void *ws, size_t have, size_t need) {
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) % 256) != 0 || have < need) return TRIA_ERR_WORKSPACE;
+  return TRIA_OK;
+}
+
+namespace {
+
+using namespace dev;
+
+constexpr int kMoveThreads = 256;
+constexpr int kPieces = kHeadDim * 2 / 16;  // 16-byte pieces of a row
+
+struct LayerPtrs {
+  uint16_t *k[TRIA_MAX_LAYERS];
+  uint16_t *v[TRIA_MAX_LAYERS];
+};
+
+// ---------------------------------------------------------------------------
+// Accepted path: row N + accepted[j] -> row N + j, j ascending.  One block
+// moves the K or the V rows of one (sequence, layer), all KV heads, in chunks
+// of kMoveU x 256 pieces: a chunk is read into registers, a barrier, written.
+// In place this is safe: accepted[j] >= j, so a later chunk's sources lie
+// above every destination already written, and within a chunk every read
+// comes before the barrier.
+// ---------------------------------------------------------------------------
+constexpr int kMoveU = 8;
+constexpr int kMoveRows = kMoveU * kMoveThreads / kPieces;  // rows of a chunk: 128
+
+struct CommitParams {
+  RowsView view;
+  LayerPtrs at;        // layers layer0 ..
+  int layer0, nl;
+  const int32_t *accepted, *n_accepted;
+  int max_accept;
+  int grow;            // lengths are updated by this call
+  uint32_t *arrived;   // [n_seq] blocks done; the last one updates the lengths and resets it
+  int32_t *status;
+};
+
+__global__ void __launch_bounds__(kMoveThreads) commit_kernel(const __grid_constant__ CommitParams p) {
+  const RowsView &v = p.view;
+  const int s = blockIdx.x / (2 * p.nl), l = (blockIdx.x / 2) % p.nl, is_v = blockIdx.x & 1;
+  const int tid = threadIdx.x, layer = p.layer0 + l;
+  const int N = view_len(v, s, layer);
+  const int n = p.n_accepted[s];
+  const int32_t *acc = p.accepted + (int64_t)s * p.max_accept;
+  const bool count_ok = n >= 0 && n <= p.max_accept;
+  bool asc = count_ok;
+  int last = -1;
+  if (count_ok) {
+    for (int j = tid; j < n; j += kMoveThreads) asc = asc && acc[j] > (j > 0 ? acc[j - 1] : -1);
+    if (n > 0) last = acc[n - 1];
+  }
+  const bool path_ok = __syncthreads_and(asc) != 0;
+  const bool ok = path_ok && N >= 0 && last < v.max_seq_len - N;
+  if (!ok) {
+    if (tid == 0) atomicOr(p.status, 1);
+  } else {
+    uint16_t *base = is_v ? p.at.v[l] : p.at.k[l];
+    int32_t *pos = (is_v || v.positions == nullptr)
+                       ? nullptr
+                       : v.positions + ((int64_t)s * v.n_layers + layer) * v.hkv * v.max_seq_len;
+    const int64_t rows = (int64_t)n * v.hkv;
+    for (int64_t r0 = 0; r0 < rows; r0 += kMoveRows) {
+      uint4 x[kMoveU];
+      int32_t xp[kMoveU];
+      uint32_t moves = 0;
+      bool bad = false;
+#pragma unroll
+      for (int u = 0; u < kMoveU; ++u) {
+        const int64_t r = r0 + (u * kMoveThreads + tid) / kPieces;
+        if (r < rows) {
+          const int j = (int)(r / v.hkv), h = (int)(r % v.hkv), a = acc[j];
+          int64_t from, to;
+          if (a != j) {
+            const bool there = view_row(v, s, h, N + a, &from) && view_row(v, s, h, N + j, &to);
+            if (there) {
+              x[u] = *reinterpret_cast<const uint4 *>(base + from + (tid % kPieces) * 8);
+              moves |= 1u << u;
+            } else {
+              bad = true;
+            }
+            if (pos != nullptr && tid % kPieces == 0) xp[u] = pos[(int64_t)h * v.max_seq_len + N + a];
+          }
+        }
+      }
+      if (bad) atomicOr(p.status, 1);
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoveU; ++u) {
+        if (!((moves >> u) & 1u)) continue;
+        const int64_t r = r0 + (u * kMoveThreads + tid) / kPieces;
+        const int j = (int)(r / v.hkv), h = (int)(r % v.hkv);
+        int64_t to;
+        view_row(v, s, h, N + j, &to);
+        *reinterpret_cast<uint4 *>(base + to + (tid % kPieces) * 8) = x[u];
+        if (pos != nullptr && tid % kPieces == 0) pos[(int64_t)h * v.max_seq_len + N + j] = xp[u];
+      }
+    }
+  }
+  if (!p.grow) return;
+  // every block of the sequence has read its length before it arrives here
+  __shared__ int s_last;
+  __syncthreads();
+  if (tid == 0) s_last = atom_add_acq_rel(p.arrived + s, 1u) == (uint32_t)(2 * p.nl - 1) ? 1 : 0;
+  __syncthreads();
+  if (!s_last) return;
+  if (tid == 0) p.arrived[s] = 0u;
+  if (!path_ok) return;
+  if (v.lens_l == 0) {
+    if (tid == 0 && ok) v.lens[s] = N + n;
+  } else {
+    for (int i = tid; i < p.nl; i += kMoveThreads) {
+      const int nl = view_len(v, s, p.layer0 + i);
+      if (nl >= 0 && last < v.max_seq_len - nl) v.lens[(int64_t)s * v.lens_s + p.layer0 + i] = nl + n;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forks.  The destinations of one source form a group, so a source row is read
+// once and written to (up to kForkDst at a time) destinations.  One block
+// copies kForkRows slots of the K or V rows of one (group, layer), all KV
+// heads; slots whose block a destination shares are skipped for it.
+// ---------------------------------------------------------------------------
+constexpr int kForkRows = 64;
+constexpr int kForkDst = 4;
+constexpr int kForkU = 8;                   // 16-byte loads in flight per thread
+constexpr int kForkBlocks = kForkRows / 8;  // paged blocks of a chunk, at most
+
+struct ForkParams {
+  RowsView view;
+  LayerPtrs at;
+  int layer0, nl;
+  int write_len;
+  int32_t *status;
+  uint16_t src[TRIA_MAX_SEQS];        // source of each group
+  uint16_t first[TRIA_MAX_SEQS + 1];  // the group's destinations: dst[first[g] .. first[g + 1])
+  uint16_t dst[TRIA_MAX_SEQS];
+};
+
+__global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constant__ ForkParams p) {
+  const RowsView &v = p.view;
+  const int g = blockIdx.z, l = blockIdx.y >> 1, is_v = blockIdx.y & 1, tid = threadIdx.x;
+  const int layer = p.layer0 + l, s = p.src[g];
+  const int d0 = p.first[g], d1 = p.first[g + 1];
+  const int N = view_len(v, s, layer);
+  if (N < 0) {
+    if (tid == 0) atomicOr(p.status, 1);
+    return;
+  }
+  if (blockIdx.x == 0 && !is_v && p.write_len && (v.lens_l != 0 || l == 0))
+    for (int d = d0 + tid; d < d1; d += kMoveThreads)
+      v.lens[(int64_t)p.dst[d] * v.lens_s + (int64_t)layer * v.lens_l] = N;
+  const int t0 = blockIdx.x * kForkRows;
+  if (t0 >= N) return;
+  const int nt = min(kForkRows, N - t0);
+  uint16_t *base = is_v ? p.at.v[l] : p.at.k[l];
+  const bool paged = v.layout == TRIA_LAYOUT_PAGED;
+  const int bs = v.block_size;
+  const int b0 = paged ? t0 / bs : 0, nb = paged ? (t0 + nt - 1) / bs - b0 + 1 : 1;
+  __shared__ int64_t s_from[kForkBlocks], s_to[kForkDst][kForkBlocks];
+  __shared__ uint32_t s_need[kForkBlocks];
+  for (int d = d0; d < d1; d += kForkDst) {
+    const int nd = min(kForkDst, d1 - d);
+    __syncthreads();
+    if (tid < nb) {
+      // where block b0 + tid of the source and of each destination begins, and
+      // which destinations need a copy of it
+      uint32_t need = 0;
+      if (!paged) {
+        s_from[0] = (int64_t)s * v.s_seq;
+        for (int i = 0; i < nd; ++i) s_to[i][0] = (int64_t)p.dst[d + i] * v.s_seq;
+        need = (1u << nd) - 1u;
+      } else {
+        const int sb = v.block_table[(int64_t)s * v.max_blocks + b0 + tid];
+        const bool s_ok = sb >= 0 && sb < v.num_blocks;
+        bool bad = !s_ok;
+        s_from[tid] = (int64_t)sb * v.s_blk;
+        for (int i = 0; i < nd; ++i) {
+          const int db = v.block_table[(int64_t)p.dst[d + i] * v.max_blocks + b0 + tid];
+          const bool d_ok = db >= 0 && db < v.num_blocks;
+          s_to[i][tid] = (int64_t)db * v.s_blk;
+          bad = bad || !d_ok;
+          if (s_ok && d_ok && db != sb) need |= 1u << i;
+        }
+        if (bad) atomicOr(p.status, 1);
+      }
+      s_need[tid] = need;
+    }
+    __syncthreads();
+    const int pieces = nt * v.hkv * kPieces;  // at most 64 x hkv x 16; hkv <= INT32_MAX / 1024 (host)
+    for (int i0 = tid; i0 < pieces; i0 += kForkU * kMoveThreads) {
+      uint4 x[kForkU];
+      int64_t off[kForkU];
+      uint32_t meta[kForkU];  // block of the chunk, and the destinations
+#pragma unroll
+      for (int u = 0; u < kForkU; ++u) {
+        const int i = i0 + u * kMoveThreads;
+        meta[u] = 0;
+        if (i < pieces) {
+          const int row = i / kPieces, t = row / v.hkv, h = row - t * v.hkv;
+          const int b = paged ? (t0 + t) / bs - b0 : 0;
+          const int in = paged ? (t0 + t) % bs : t0 + t;
+          const uint32_t need = s_need[b];
+          off[u] = (int64_t)h * v.s_head + (int64_t)in * v.s_tok + (i % kPieces) * 8;
+          meta[u] = need | ((uint32_t)b << 8);
+          if (need) x[u] = __ldcs(reinterpret_cast<const uint4 *>(base + s_from[b] + off[u]));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kForkU; ++u)
+#pragma unroll
+        for (int k = 0; k < kForkDst; ++k)
+          if ((meta[u] >> k) & 1u)
+            *reinterpret_cast<uint4 *>(base + s_to[k][meta[u] >> 8] + off[u]) = x[u];
+    }
+  }
+  if (is_v || v.positions == nullptr) return;
+  const int64_t unit = (int64_t)v.hkv * v.max_seq_len;
+  const int32_t *from = v.positions + ((int64_t)s * v.n_layers + layer) * unit;
+  for (int i = tid; i < nt * v.hkv; i += kMoveThreads) {
+    const int64_t o = (int64_t)(i / nt) * v.max_seq_len + t0 + i % nt;
+    const int32_t x = from[o];
+    for (int d = d0; d < d1; ++d)
+      v.positions[((int64_t)p.dst[d] * v.n_layers + layer) * unit + o] = x;
+  }
+}
+
+void layer_ptrs(const tria_cache_view *c, int layer0, int layer1, LayerPtrs *at) {
+  for (int l = layer0; l < layer1; ++l) {
+    at->k[l - layer0] = static_cast<uint16_t *>(c->k_layers[l]);
+    at->v[l - layer0] = static_cast<uint16_t *>(c->v_layers[l]);
+  }
+}
+
+size_t commit_ws_bytes(const tria_cache_view *c) {
+  return kHeaderBytes + ((size_t)c->n_seq * 4 + 255) / 256 * 256;
+}
+
+int32_t *status_of(void *ws) { return reinterpret_cast<int32_t *>(static_cast<unsigned char *>(ws) + 4); }
+
+// lengths move with the call over the last layer, or with their own layer
+bool moves_lens(const RowsView &v, int layer1) { return v.lens_l != 0 || layer1 == v.n_layers; }
+
+}  // namespace
+}  // namespace tria
+
+using namespace tria;
+
+extern "C" {
+
+tria_status tria_commit_workspace_size(const tria_stats *stats, const tria_cache_view *cache, size_t *bytes) {
+  if (stats == nullptr || cache == nullptr || bytes == nullptr) return TRIA_ERR_INVALID_ARG;
+  if (cache->n_seq < 1 || cache->n_seq > TRIA_MAX_SEQS) return TRIA_ERR_INVALID_ARG;
+  *bytes = commit_ws_bytes(cache);
+  return TRIA_OK;
+}
+
+tria_status tria_tree_commit(const tria_stats *stats, const tria_cache_view *cache,
+                             const int32_t *accepted, const int32_t *n_accepted, int max_accept,
+                             int layer0, int layer1, void *ws, size_t ws_bytes, tria_stream_t stream) {
+  tria_model_desc d;
+  CommitParams p{};
+  const tria_status st = make_rows_view(stats, cache, layer0, layer1, &d, &p.view);
+  if (st != TRIA_OK) return st;
+  if (accepted == nullptr || n_accepted == nullptr || max_accept < 1 ||
+      (reinterpret_cast<uintptr_t>(accepted) & 3u) || (reinterpret_cast<uintptr_t>(n_accepted) & 3u))
+    return TRIA_ERR_INVALID_ARG;
+  const tria_status sw = check_header_workspace(ws, ws_bytes, commit_ws_bytes(cache));
+  if (sw != TRIA_OK) return sw;
+  layer_ptrs(cache, layer0, layer1, &p.at);
+  p.layer0 = layer0;
+  p.nl = layer1 - layer0;
+  p.accepted = accepted;
+  p.n_accepted = n_accepted;
+  p.max_accept = max_accept;
+  p.grow = moves_lens(p.view, layer1) ? 1 : 0;
+  p.arrived = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
+  p.status = status_of(ws);
+  const unsigned blocks = (unsigned)cache->n_seq * (unsigned)p.nl * 2u;
+  commit_kernel<<<blocks, kMoveThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+}
+
+tria_status tria_fork_workspace_size(const tria_stats *stats, const tria_cache_view *cache, size_t *bytes) {
+  if (stats == nullptr || cache == nullptr || bytes == nullptr) return TRIA_ERR_INVALID_ARG;
+  *bytes = kHeaderBytes;
+  return TRIA_OK;
+}
+
+tria_status tria_fork_sequences(const tria_stats *stats, const tria_cache_view *cache, const int32_t *src,
+                                const int32_t *dst, int n_fork, int layer0, int layer1, void *ws,
+                                size_t ws_bytes, tria_stream_t stream) {
+  tria_model_desc d;
+  ForkParams p;
+  std::memset(&p, 0, sizeof(p));
+  const tria_status st = make_rows_view(stats, cache, layer0, layer1, &d, &p.view);
+  if (st != TRIA_OK) return st;
+  if (d.n_kv_heads > INT32_MAX / (kForkRows * kPieces)) return TRIA_ERR_UNSUPPORTED;
+  if (n_fork < 0 || n_fork > TRIA_MAX_SEQS || (n_fork > 0 && (src == nullptr || dst == nullptr)))
+    return TRIA_ERR_INVALID_ARG;
+  uint16_t count[TRIA_MAX_SEQS] = {};  // destinations of each source
+  bool is_dst[TRIA_MAX_SEQS] = {};
+  for (int i = 0; i < n_fork; ++i) {
+    if (src[i] < 0 || src[i] >= cache->n_seq || dst[i] < 0 || dst[i] >= cache->n_seq || is_dst[dst[i]])
+      return TRIA_ERR_INVALID_ARG;
+    is_dst[dst[i]] = true;
+    ++count[src[i]];
+  }
+  int groups = 0, filled = 0;
+  uint16_t at[TRIA_MAX_SEQS];  // next free place of each source's group
+  for (int s = 0; s < cache->n_seq; ++s) {
+    if (count[s] == 0) continue;
+    if (is_dst[s]) return TRIA_ERR_INVALID_ARG;
+    p.src[groups] = (uint16_t)s;
+    p.first[groups++] = at[s] = (uint16_t)filled;
+    filled += count[s];
+  }
+  p.first[groups] = (uint16_t)filled;
+  for (int i = 0; i < n_fork; ++i) p.dst[at[src[i]]++] = (uint16_t)dst[i];
+  const tria_status sw = check_header_workspace(ws, ws_bytes, kHeaderBytes);
+  if (sw != TRIA_OK) return sw;
+  if (n_fork == 0) return TRIA_OK;
+  layer_ptrs(cache, layer0, layer1, &p.at);
+  p.layer0 = layer0;
+  p.nl = layer1 - layer0;
+  p.write_len = moves_lens(p.view, layer1) ? 1 : 0;
+  p.status = status_of(ws);
+  const dim3 grid((unsigned)((cache->max_seq_len + (int64_t)kForkRows - 1) / kForkRows), 2u * p.nl,
+                  (unsigned)groups);
+  fork_kernel<<<grid, kMoveThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+}
+
+}  // extern "C"
