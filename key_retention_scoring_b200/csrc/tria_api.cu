@@ -358,6 +358,21 @@ LensParams make_lens(const Geom &g, const tria_cache_view *c, int layer0, int la
 
 }  // namespace
 
+bool encode_rows_map(CUtensorMap *map, const void *base, const uint64_t (&dims)[4],
+                     const int64_t (&strides)[3], const uint32_t (&box)[4]) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t bytes[3];
+  for (int i = 0; i < 3; ++i) {
+    // a dimension of extent 1 never advances: any stride that the encoder takes stands for it
+    bytes[i] = dims[i + 1] == 1 ? 256 : (cuuint64_t)strides[i] * 2;
+  }
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, bytes, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 WsLayout ws_layout(const Geom &g) {
   WsLayout w{};
   size_t off = 0;

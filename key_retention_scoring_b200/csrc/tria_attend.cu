@@ -1,111 +1,981 @@
-// Attention of many query rows at once: whole prompts, causal, packed
-// (tria_prompt_attention), and drafted tokens over the cached rows of a layer
-// (tria_tree_attention).
+// Attention of many query rows at once on the sm_100a tensor cores: whole
+// prompts, causal, packed (tria_prompt_attention), and drafted tokens over the
+// cached rows of a layer (tria_tree_attention).
 //
-// Query row i (token i of sequence s, query head qh, KV head h = qh / G) sees
-// the keys j < ctx + T of its sequence for which
+// Query row (token i, query head qh of KV head h = qh / G) of sequence s sees
+// the keys j < ctx + T for which
 //   j < ctx, or j - ctx <= i (a chain), or bit j - ctx of its mask is set
 // (prompts: ctx = 0, T = the sequence's length):
 //   out_i = sum_j softmax(scale q_i.k_j)_j v_j,  lse_i = log sum_j exp(scale q_i.k_j).
 //
-// One warp per (token, query head), a key after the other with a running
-// maximum and sum; each lane holds 4 of the 128 dims.
+// Rows of a KV head's G query heads share its keys, so a tile of 128 rows is
+// 128 / G tokens x G heads (one TMA box), and two tiles are in flight:
+//   DUALQ: two tiles of rows against the same key blocks (prompts; more than
+//          128 rows of drafted tokens);
+//   DUALK: one tile of rows, its even and odd key blocks (at most 128 rows:
+//          both halves of the SM stay busy although there is one tile).
+// Roles (one CTA per SM, persistent):
+//   warps 0-3, 4-7  softmax of tile (or half) 0 and 1, one thread per row:
+//                   S from tensor memory, running maximum and sum in fp32,
+//                   P as bf16 back over S, the output at the end;
+//   warp 8          one lane issues tcgen05.mma: S = Q K^T (both in shared
+//                   memory), O += P V (P in tensor memory, V as it lies,
+//                   MN-major); while one tile's softmax runs, the other's
+//                   products do;
+//   warp 9          items of work, and TMA loads of Q and the K/V ring.
+// P is rounded to bf16: the second product needs 16-bit operands, the output
+// is rounded to bf16 anyway, and l sums the unrounded weights.
+//
+// What no row may see.  Masked logits become -inf, so masked weights are 0;
+// but 0 x inf and 0 x NaN are NaN, and V rows in a masked place may hold
+// anything (later tokens, other sequences, unused slots).  In blocks that hold
+// masked places the softmax warps therefore look V over in shared memory
+// before the product reads it, replace what is not finite by 0 and note it;
+// the epilogue then adds those values to the rows that do see them.
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "tria_device.cuh"
+#include "tria_tc.cuh"
 
 namespace tria {
 namespace {
 
 using namespace dev;
+using namespace tc;
 
-constexpr int kWarps = 8;
+constexpr int kBN = 128;                       // keys per block
+constexpr int kTile = 2 * kHalfBlock;          // bytes of 128 rows x 128 bf16
+constexpr int kSoftWarps = 8;
+constexpr int kIssueWarp = 8, kLoadWarp = 9;
+constexpr int kAtThreads = 320;
+constexpr int kPacked = 2;                     // LAYOUT of prompts, next to the cache layouts
+constexpr uint32_t kColS = 0, kColO = 256;     // tensor-memory columns: S (and P) of half t at 128 t, O after them
+constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum of a row (base 2) moves only when a block exceeds it by
+// more than this, so most blocks leave O in tensor memory alone; weights stay
+// below 2^8, well inside fp32 and bf16.
+constexpr float kSlack = 8.f;
 
 struct AttendParams {
-  const uint16_t *q, *k, *v;
-  int64_t q_tok, q_head;
-  int64_t k_tok, k_head, v_tok, v_head;  // packed rows
-  RowsView view;                         // cached rows
-  int layer;
-  int cached;
-  const int32_t *starts;
-  int n_seq, hq, hkv, g;
+  CUtensorMap qmap, kmap, vmap;
+  const uint16_t *v;
+  int64_t v_tok, v_head;                       // packed rows
+  RowsView view;                               // cached rows
+  int layer, n_seq, hq, hkv, g, g_log2;
   int64_t n_tokens;
+  const int32_t *starts;
   int max_draft;
   const uint32_t *mask;
   int mask_words;
-  float scale;
+  float qscale;                                // scale log2(e): base-2 logits
   uint16_t *out;
   float *lse;
+  float *part_o, *part_ml;                     // [2 grid][rows][128], [2 grid][rows][2]
   int32_t *status;
 };
 
-__device__ __forceinline__ float4 row4(const uint16_t *p, int lane) {
-  const uint2 w = *reinterpret_cast<const uint2 *>(p + 4 * lane);
-  return make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y));
-}
+// One piece of work: rows of tokens [tok0, ..) of (s, h) against key blocks [kb0, kb1).
+struct Item {
+  int s, h, tok0, T, ctx, kb0, kb1, slot;      // slot: -1 writes the output, else a partial
+  int64_t row0;                                // first row of the sequence in q and out
+};
 
-__global__ void __launch_bounds__(32 * kWarps) attend_kernel(const __grid_constant__ AttendParams p) {
-  const int s = blockIdx.y, qh = blockIdx.z, h = qh / p.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <bool DUALK>
+struct AtCfg {
+  static constexpr int QT = DUALK ? 1 : 2;           // tiles of rows
+  static constexpr int ROWS = 128 * QT;
+  static constexpr int ST = 5;                       // ring stages (K or V tiles)
+};
+
+template <bool DUALK>
+struct AtSmem {
+  alignas(1024) uint8_t q[AtCfg<DUALK>::QT][kTile];
+  alignas(1024) uint8_t kv[AtCfg<DUALK>::ST][kTile];
+  alignas(8) uint64_t kv_full[AtCfg<DUALK>::ST], kv_empty[AtCfg<DUALK>::ST];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], it_full[2], it_empty[2], ml_full, o_read, drain;
+  Item item[2];
+  float ml[DUALK ? 2 : 1][2][DUALK ? 128 : 1];
+  volatile int poison[2];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+};
+
+// ---------------------------------------------------------------------------
+// what a sequence holds, and the order of the work
+// ---------------------------------------------------------------------------
+// T, ctx and first row of sequence s; T = 0 for one that is empty or bad (*bad).
+template <int LAYOUT>
+__device__ __forceinline__ void seq_of(const AttendParams &p, int s, int &T, int &ctx, int64_t &row0, bool &bad) {
   const int64_t a = p.starts[s], b = p.starts[s + 1];
-  bool ok = a >= 0 && b >= a && b <= p.n_tokens;
-  int ctx = 0;
-  if (ok && b > a && p.cached) {
+  T = 0;
+  ctx = 0;
+  row0 = a;
+  bad = a < 0 || b < a || b > p.n_tokens;
+  if (bad || b == a) return;
+  if (LAYOUT != kPacked) {
     ctx = view_len(p.view, s, p.layer);
-    ok = ctx >= 0 && b - a <= p.max_draft && b - a <= p.view.max_seq_len - ctx;
+    bad = ctx < 0 || b - a > p.max_draft || b - a > p.view.max_seq_len - ctx;
+    if (bad) return;
   }
-  if (!ok) {
-    if (threadIdx.x == 0) atomicOr(p.status, 1);
-    return;
+  T = (int)(b - a);
+}
+
+// key blocks that tokens [.., tok_end) of a sequence see
+__device__ __forceinline__ int key_blocks(const AttendParams &p, int ctx, int T, int tok_end) {
+  const int n = ctx + (p.mask != nullptr ? T : min(T, tok_end));
+  return (n + kBN - 1) / kBN;
+}
+
+// key blocks of all (KV head, tile of ROWS rows) units of a sequence
+template <int ROWS>
+__device__ __forceinline__ int64_t seq_blocks(const AttendParams &p, int ctx, int T) {
+  const int tpi = ROWS >> p.g_log2, tiles = (T + tpi - 1) / tpi;
+  int64_t n = 0;
+  if (p.mask != nullptr) {
+    n = (int64_t)tiles * key_blocks(p, ctx, T, T);
+  } else {
+    for (int t = 0; t < T; t += tpi) n += key_blocks(p, ctx, T, t + tpi);
   }
-  const int T = (int)(b - a);
-  for (int i = blockIdx.x * kWarps + warp; i < T; i += gridDim.x * kWarps) {
-    const float4 q = row4(p.q + (a + i) * p.q_tok + (int64_t)qh * p.q_head, lane);
-    const uint32_t *bits = p.mask ? p.mask + (a + i) * p.mask_words : nullptr;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int n = ctx + (bits ? T : i + 1);
-    for (int j = 0; j < n; ++j) {
-      if (bits && j >= ctx && !((bits[(j - ctx) >> 5] >> ((j - ctx) & 31)) & 1u)) continue;
-      float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-      if (p.cached) {
-        int64_t off;
-        if (view_row(p.view, s, h, j, &off)) {
-          k = row4(p.k + off, lane);
-          v = row4(p.v + off, lane);
-        }
-      } else {
-        k = row4(p.k + (a + j) * p.k_tok + (int64_t)h * p.k_head, lane);
-        v = row4(p.v + (a + j) * p.v_tok + (int64_t)h * p.v_head, lane);
-      }
-      float z = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+  return n * p.hkv;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
-      for (int x = 16; x >= 1; x >>= 1) z += __shfl_xor_sync(kFull, z, x);
-      z *= p.scale;
-      const float mn = fmaxf(m, z), f = expf(m - mn), e = expf(z - mn);
-      l = fmaf(l, f, e);
-      o.x = fmaf(o.x, f, e * v.x);
-      o.y = fmaf(o.y, f, e * v.y);
-      o.z = fmaf(o.z, f, e * v.z);
-      o.w = fmaf(o.w, f, e * v.w);
-      m = mn;
+  for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  return x;
+}
+
+// Prompts: tiles of all sequences, those with the most keys first (tile t of a
+// sequence sees t + 1 tiles of keys), all KV heads of a tile side by side; the
+// CTAs take them in turn, forth and back, which evens the sums out.
+template <bool DUALK>
+struct PromptCursor {
+  int64_t n_items;
+  int tmax, round;
+
+  __device__ int tpi(const AttendParams &p) const { return AtCfg<DUALK>::ROWS >> p.g_log2; }
+
+  // tiles with index >= t, over all sequences
+  __device__ int64_t from(const AttendParams &p, int t, int lane) const {
+    int64_t n = 0;
+    for (int s = lane; s < p.n_seq; s += 32) {
+      int T, ctx;
+      int64_t row0;
+      bool bad;
+      seq_of<kPacked>(p, s, T, ctx, row0, bad);
+      n += max(0, (T + tpi(p) - 1) / tpi(p) - t);
     }
-    const float inv = n > 0 && l != 0.f ? 1.f / l : 0.f;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    uint2 w;
-    w.x = *reinterpret_cast<const uint32_t *>(&lo);
-    w.y = *reinterpret_cast<const uint32_t *>(&hi);
-    *reinterpret_cast<uint2 *>(p.out + ((a + i) * p.hq + qh) * 128 + 4 * lane) = w;
-    if (p.lse != nullptr && lane == 0) p.lse[(a + i) * p.hq + qh] = m + logf(l);
+    return warp_sum(n);
+  }
+
+  __device__ void init(const AttendParams &p, int lane) {
+    int most = 0;
+    bool any_bad = false;
+    for (int s = lane; s < p.n_seq; s += 32) {
+      int T, ctx;
+      int64_t row0;
+      bool bad;
+      seq_of<kPacked>(p, s, T, ctx, row0, bad);
+      any_bad = any_bad || bad;
+      most = max(most, (T + tpi(p) - 1) / tpi(p));
+    }
+    if (any_bad && blockIdx.x == 0) atomicOr(p.status, 1);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
+    tmax = most;
+    n_items = from(p, 0, lane) * p.hkv;
+    round = 0;
+  }
+
+  __device__ bool next(const AttendParams &p, int lane, Item &x) {
+    const int64_t grid = gridDim.x, b = blockIdx.x;
+    const int64_t k = round * grid + ((round & 1) ? grid - 1 - b : b);
+    ++round;
+    if (k >= n_items) return false;  // later rounds begin behind k
+    const int64_t pos = k / p.hkv;
+    x.h = (int)(k % p.hkv);
+    int lo = 0, hi = tmax - 1;  // the largest t with from(t) > pos
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (from(p, mid, lane) > pos) lo = mid; else hi = mid - 1;
+    }
+    int64_t rem = pos - from(p, lo + 1, lane);
+    x.s = -1;
+    for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+      const int s = s0 + lane;
+      int T = 0, ctx;
+      int64_t row0;
+      bool bad;
+      if (s < p.n_seq) seq_of<kPacked>(p, s, T, ctx, row0, bad);
+      const uint32_t has = __ballot_sync(kFull, (T + tpi(p) - 1) / tpi(p) > lo);
+      const int cnt = __popc(has);
+      if (rem < cnt) {
+        x.s = s0 + __fns(has, 0, (int)rem + 1);
+        break;
+      }
+      rem -= cnt;
+    }
+    bool bad;
+    seq_of<kPacked>(p, x.s, x.T, x.ctx, x.row0, bad);
+    x.tok0 = lo * tpi(p);
+    x.kb0 = 0;
+    x.kb1 = key_blocks(p, 0, x.T, x.tok0 + tpi(p));
+    x.slot = -1;
+    return true;
+  }
+};
+
+// Drafted tokens: the key blocks of all units (sequence, KV head, tile of
+// rows) in one line, cut into one piece of equal length per CTA.  A unit that
+// lies in several pieces is put together from partials by combine_kernel.
+template <bool DUALK, int LAYOUT>
+struct TreeCursor {
+  int64_t pos, end, ub;  // blocks of this CTA still to do; where the unit begins
+  int s, h, tok0, T, ctx, pieces;
+  int64_t row0;
+
+  static __device__ int64_t total(const AttendParams &p, int lane, bool &any_bad) {
+    int64_t n = 0;
+    any_bad = false;
+    for (int s = lane; s < p.n_seq; s += 32) {
+      int T, ctx;
+      int64_t row0;
+      bool bad;
+      seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
+      any_bad = any_bad || bad;
+      n += seq_blocks<AtCfg<DUALK>::ROWS>(p, ctx, T);
+    }
+    return warp_sum(n);
+  }
+
+  __device__ void init(const AttendParams &p, int lane) {
+    bool any_bad;
+    const int64_t all = total(p, lane, any_bad);
+    if (any_bad && blockIdx.x == 0) atomicOr(p.status, 1);
+    const int64_t w = (all + gridDim.x - 1) / gridDim.x;
+    pos = blockIdx.x * w;
+    end = min(all, pos + w);
+    pieces = 0;
+    if (pos >= end) return;
+    // the sequence that holds block `pos`
+    int64_t before = 0;
+    for (int s0 = 0;; s0 += 32) {
+      int64_t c = 0;
+      if (s0 + lane < p.n_seq) {
+        int t, x;
+        int64_t r;
+        bool bad;
+        seq_of<LAYOUT>(p, s0 + lane, t, x, r, bad);
+        c = seq_blocks<AtCfg<DUALK>::ROWS>(p, x, t);
+      }
+      int64_t incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t past = __ballot_sync(kFull, before + incl > pos);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        s = s0 + at;
+        ub = before + __shfl_sync(kFull, incl - c, at);
+        break;
+      }
+      before += __shfl_sync(kFull, incl, 31);
+    }
+    load(p);
+    while (ub + unit(p) <= pos) step(p);
+  }
+
+  __device__ void load(const AttendParams &p) {
+    bool bad;
+    seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
+    h = tok0 = 0;
+  }
+  __device__ int tpi(const AttendParams &p) const { return AtCfg<DUALK>::ROWS >> p.g_log2; }
+  __device__ int unit(const AttendParams &p) const { return key_blocks(p, ctx, T, tok0 + tpi(p)); }
+  __device__ void step(const AttendParams &p) {
+    ub += unit(p);
+    tok0 += tpi(p);
+    if (tok0 < T) return;
+    tok0 = 0;
+    if (++h < p.hkv) return;
+    do {
+      ++s;
+      load(p);
+    } while (T == 0);  // a block at or behind ub exists, so a later sequence has one
+  }
+
+  __device__ bool next(const AttendParams &p, int lane, Item &x) {
+    if (pos >= end) return false;
+    const int nb = unit(p);
+    x.s = s;
+    x.h = h;
+    x.tok0 = tok0;
+    x.T = T;
+    x.ctx = ctx;
+    x.row0 = row0;
+    x.kb0 = (int)(pos - ub);
+    x.kb1 = (int)(min(end, ub + nb) - ub);
+    x.slot = x.kb1 - x.kb0 == nb ? -1 : 2 * (int)blockIdx.x + (pieces > 0 ? 1 : 0);
+    pos = ub + x.kb1;
+    ++pieces;
+    if (pos < end) step(p);
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// loads
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+template <bool DUALK, int LAYOUT, class Cursor>
+__device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, const WaitCtl wc) {
+  using Cfg = AtCfg<DUALK>;
+  constexpr int ST = Cfg::ST;
+  // drafted rows read the cache once; prompts read their keys again for later tiles
+  const uint64_t pol = LAYOUT != kPacked && DUALK ? evict_first_policy() : normal_policy();
+  const uint64_t qpol = normal_policy();
+  Cursor cur;
+  cur.init(p, lane);
+  int it = 0, li = 0;
+  bool ok = true;
+  Item x{};
+  auto wait = [&](uint64_t *bar, int phase) {
+    bool good = true;
+    if (lane == 0) good = mbar_wait(bar, (uint32_t)(phase & 1), wc);
+    return __shfl_sync(kFull, good ? 1 : 0, 0) != 0;
+  };
+  int next_blk = -1, next_j = -1;
+  auto table = [&](int j) {  // this lane's block id of key block j of the item
+    const int bs = p.view.block_size, t = (x.kb0 + j) * kBN + (lane >> 1) * bs;
+    return (lane >> 1) < kBN / bs && t < x.ctx + x.T
+               ? __ldg(p.view.block_table + (int64_t)x.s * p.view.max_blocks + t / bs)
+               : 0;
+  };
+  auto load = [&](bool is_v, int j, int n) -> bool {
+    const int stage = li % ST;
+    if (li >= ST && !wait(&sm.kv_empty[stage], li / ST - 1)) return false;
+    const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
+    const uint32_t dst = smem_u32(&sm.kv[stage][0]);
+    const int slot0 = (x.kb0 + j) * kBN;
+    if (LAYOUT != TRIA_LAYOUT_PAGED) {
+      if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[stage], kTile);
+      __syncwarp();
+      if (lane < 2) {
+        if (LAYOUT == kPacked)
+          tma_load_4d(dst + lane * kHalfBlock, map, lane * 64, (int)x.row0 + slot0, x.h, 0, &sm.kv_full[stage], pol);
+        else
+          tma_load_4d(dst + lane * kHalfBlock, map, lane * 64, slot0, x.h, x.s, &sm.kv_full[stage], pol);
+      }
+    } else {
+      // one box per page and 64-dim half; pages behind the last row stay unread
+      // (what the stage holds there is masked)
+      const int bs = p.view.block_size, at = lane >> 1, half = lane & 1;
+      const bool valid = at < kBN / bs && slot0 + at * bs < x.ctx + x.T;
+      const int blk = !is_v && next_j == j ? next_blk : table(j);
+      const int boxes = __popc(__ballot_sync(kFull, valid));
+      if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[stage], (uint32_t)(boxes * bs * 128));
+      __syncwarp();
+      if (valid)
+        tma_load_4d(dst + half * kHalfBlock + at * bs * 128, map, half * 64, x.h, 0, blk, &sm.kv_full[stage], pol);
+      if (!is_v) {
+        next_j = j + 1 < n ? j + 1 : -1;
+        if (next_j >= 0) next_blk = table(next_j);
+      }
+    }
+    ++li;
+    return true;
+  };
+  for (;;) {
+    const bool more = cur.next(p, lane, x);
+    const int slot = it & 1;
+    if (it >= 2 && !(ok = wait(&sm.it_empty[slot], (it >> 1) - 1))) break;
+    if (lane == 0) {
+      if (!more) x.kb1 = -1;
+      sm.item[slot] = x;
+      mbar_arrive(&sm.it_full[slot]);
+    }
+    ++it;
+    if (!more) break;
+    next_j = -1;
+    if (it > 1 && !(ok = wait(&sm.q_empty, it - 2))) break;
+    if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, Cfg::QT * kTile);
+    __syncwarp();
+    if (lane < 2 * Cfg::QT) {
+      const int t = lane >> 1, half = lane & 1;
+      tma_load_4d(smem_u32(&sm.q[t][half * kHalfBlock]), &p.qmap, half * 64, x.h << p.g_log2,
+                  (int)x.row0 + x.tok0 + t * (kRows >> p.g_log2), 0, &sm.q_full, qpol);
+    }
+    const int n = x.kb1 - x.kb0;
+    // in the order in which mma_role uses them
+    if (DUALK) {
+      ok = load(false, 0, n) && (n < 2 || load(false, 1, n));
+      for (int j = 0; ok && j < n; ++j) ok = load(true, j, n) && (j + 2 >= n || load(false, j + 2, n));
+    } else {
+      for (int j = 0; ok && j < n; ++j) ok = load(false, j, n) && load(true, j, n);
+    }
+    if (!ok) break;
+  }
+  if (!ok && lane == 0) {
+    // aborted: loads still in flight must land before the block exits
+    for (int j = li > ST ? li - ST : 0; j < li; ++j) mbar_drain(&sm.kv_full[j % ST], (j / ST) & 1, wc.status);
+    if (it > 0) mbar_drain(&sm.q_full, (it - 1) & 1, wc.status);
   }
 }
 
+// ---------------------------------------------------------------------------
+// products (one lane)
+// ---------------------------------------------------------------------------
+// V tile as the B operand of O += P V: N = dims, which lie contiguous (MN-
+// major): 128-byte swizzle, the two 64-dim halves kHalfBlock bytes apart
+// (leading offset), 8-key groups 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(kHalfBlock >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+constexpr uint32_t kIdescS = idesc_bf16_m128_n(kBN);
+constexpr uint32_t kIdescO = idesc_bf16_m128_n(kHeadDim) | (1u << 16);  // B is MN-major
+
+template <bool DUALK>
+__device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, const WaitCtl wc) {
+  using Cfg = AtCfg<DUALK>;
+  constexpr int ST = Cfg::ST;
+  int li = 0, pc[2] = {0, 0};
+  bool ok = true, issued = false;
+  auto kv_wait = [&](int i) { return mbar_wait(&sm.kv_full[i % ST], (uint32_t)((i / ST) & 1), wc); };
+  auto qk = [&](int t, int i) {
+    const uint64_t a = sw128_desc(smem_u32(&sm.q[DUALK ? 0 : t][0])), b = sw128_desc(smem_u32(&sm.kv[i % ST][0]));
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint32_t o = (uint32_t)((s >> 2) * kHalfBlock + (s & 3) * 32) >> 4;
+      mma_bf16(tmem + kColS + 128u * t, a + o, b + o, kIdescS, s > 0 ? 1u : 0u);
+    }
+    issued = true;
+  };
+  auto pv = [&](int t, int i, bool first) {
+    const uint64_t b = v_desc(smem_u32(&sm.kv[i % ST][0]));
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      mma_bf16_ta(tmem + kColO + 128u * t, tmem + kColS + 128u * t + 8u * s, b + (uint64_t)((s * 2048) >> 4), kIdescO,
+                  first && s == 0 ? 0u : 1u);
+  };
+  auto p_wait = [&](int t) {
+    const bool good = mbar_wait(&sm.p_full[t], (uint32_t)(pc[t] & 1), wc);
+    ++pc[t];
+    tc_fence_after();
+    return good;
+  };
+  for (int it = 0; ok; ++it) {
+    if (!(ok = mbar_wait(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc))) break;
+    const int n = sm.item[it & 1].kb1 - sm.item[it & 1].kb0;
+    const bool end = sm.item[it & 1].kb1 < 0;
+    mbar_arrive(&sm.it_empty[it & 1]);
+    if (end) break;
+    if (!(ok = mbar_wait(&sm.q_full, (uint32_t)(it & 1), wc))) break;
+    if (DUALK) {
+      for (int t = 0; t < 2 && t < n; ++t) {
+        if (!(ok = kv_wait(li))) break;
+        tc_fence_after();
+        qk(t, li);
+        mma_commit(&sm.kv_empty[li % ST]);
+        mma_commit(&sm.s_full[t]);
+        ++li;
+      }
+      if (ok && n <= 2) mma_commit(&sm.q_empty);
+      for (int j = 0; ok && j < n; ++j) {
+        const int t = j & 1;
+        if (!(ok = kv_wait(li) && p_wait(t))) break;
+        pv(t, li, j < 2);
+        mma_commit(&sm.kv_empty[li % ST]);
+        ++li;
+        if (j + 2 < n) {
+          if (!(ok = kv_wait(li))) break;
+          qk(t, li);
+          mma_commit(&sm.kv_empty[li % ST]);
+          mma_commit(&sm.s_full[t]);
+          ++li;
+          if (j + 3 == n) mma_commit(&sm.q_empty);
+        } else {
+          mma_commit(&sm.o_full[t]);
+        }
+      }
+    } else {
+      if (!(ok = kv_wait(li))) break;
+      tc_fence_after();
+      for (int t = 0; t < 2; ++t) {
+        qk(t, li);
+        mma_commit(&sm.s_full[t]);
+      }
+      mma_commit(&sm.kv_empty[li % ST]);
+      ++li;
+      if (n == 1) mma_commit(&sm.q_empty);
+      for (int j = 0; ok && j < n; ++j) {
+        const int vi = li, ki = li + 1;
+        if (!(ok = kv_wait(vi))) break;
+        for (int t = 0; t < 2; ++t) {
+          if (!(ok = p_wait(t))) break;
+          pv(t, vi, j == 0);
+          if (t == 1) mma_commit(&sm.kv_empty[vi % ST]);
+          if (j + 1 < n) {
+            if (t == 0 && !(ok = kv_wait(ki))) break;
+            qk(t, ki);
+            mma_commit(&sm.s_full[t]);
+            if (t == 1) mma_commit(&sm.kv_empty[ki % ST]);
+          } else {
+            mma_commit(&sm.o_full[t]);
+          }
+        }
+        li += j + 1 < n ? 2 : 1;
+        if (j + 2 == n) mma_commit(&sm.q_empty);
+      }
+    }
+  }
+  // the products already issued must land before the tensor memory is freed
+  if (issued) {
+    mma_commit(&sm.drain);
+    mbar_drain(&sm.drain, 0, wc.status);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// softmax and output
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// (a0, a1) * b + c on both halves
+__device__ __forceinline__ void fma2(float &a0, float &a1, float b, float c) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %3};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b), "f"(c));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ bool bf16_not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
+
+// Replaces what is not finite in the V tile by 0 (the 128 threads of a softmax
+// group); true where this thread found something.  x * 0 + acc keeps a NaN, so
+// one bf16x2 multiply-add per two values tells whether to look closer.
+__device__ __forceinline__ bool clean_v(uint8_t *tile, int tid, volatile int *poison, int mark) {
+  uint32_t acc = 0;
+#pragma unroll
+  for (int i = 0; i < kTile / 16 / 128; ++i) {
+    const uint4 w = lds128(tile + (i * 128 + tid) * 16);
+    for (uint32_t x : {w.x, w.y, w.z, w.w})
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+  }
+  if ((acc & 0x7fff7fffu) == 0) return false;
+  *poison = mark;
+  __threadfence_block();
+  for (int i = 0; i < kTile / 16 / 128; ++i) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(tile + (i * 128 + tid) * 16);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t x = w[e];
+      const uint32_t y = (bf16_not_finite(x) ? 0u : x & 0xffffu) | (bf16_not_finite(x >> 16) ? 0u : x & 0xffff0000u);
+      if (y != x) w[e] = y;
+    }
+  }
+  return true;
+}
+
+// Bit c: this row may see key k0 + c (c < 32).
+__device__ __forceinline__ uint32_t sees(const AttendParams &p, const Item &x, int tok, int k0) {
+  if (tok >= x.T) return 0u;
+  const int rel = k0 - x.ctx;  // drafted row of the first key
+  int n;                       // keys [k0, k0 + n) exist (and a chain's row sees them all)
+  if (p.mask == nullptr) {
+    n = tok + 1 - rel;
+  } else {
+    n = x.T - rel;
+  }
+  if (n <= 0) return 0u;
+  uint32_t bits = n >= 32 ? ~0u : (1u << n) - 1u;
+  if (p.mask != nullptr && rel > -32) {
+    const uint32_t *m = p.mask + (x.row0 + tok) * p.mask_words;
+    if (rel < 0) {
+      bits &= (m[0] << -rel) | ((1u << -rel) - 1u);
+    } else {
+      const int w = rel >> 5;
+      const uint32_t lo = w < p.mask_words ? m[w] : 0u, hi = w + 1 < p.mask_words ? m[w + 1] : 0u;
+      bits &= __funnelshift_r(lo, hi, rel & 31);
+    }
+  }
+  return bits;
+}
+
+// First key of the item's blocks that hold masked places.
+__device__ __forceinline__ bool block_masked(const AttendParams &p, const Item &x, int k0) {
+  return p.mask != nullptr ? k0 + kBN > x.ctx : k0 + kBN - 1 > x.ctx + x.tok0;
+}
+
+// v_j that are not finite, of the masked blocks' keys that this row sees, added to o (dims d0 .. d0 + 31).
+template <int LAYOUT>
+__device__ __noinline__ void add_not_finite(const AttendParams &p, const Item &x, int tok, int d0, float (&o)[32]) {
+  if (tok >= x.T) return;
+  for (int kb = x.kb0; kb < x.kb1; ++kb) {
+    if (!block_masked(p, x, kb * kBN)) continue;
+    for (int k0 = kb * kBN; k0 < kb * kBN + kBN; k0 += 32) {
+      uint32_t bits = sees(p, x, tok, k0);
+      while (bits) {
+        const int j = k0 + __ffs(bits) - 1;
+        bits &= bits - 1u;
+        const uint16_t *v = p.v;
+        if (LAYOUT == kPacked) {
+          v += (x.row0 + j) * p.v_tok + (int64_t)x.h * p.v_head;
+        } else {
+          int64_t off;
+          if (!view_row(p.view, x.s, x.h, j, &off)) continue;
+          v += off;
+        }
+#pragma unroll
+        for (int d = 0; d < 32; ++d) {
+          const uint32_t y = v[d0 + d];
+          if (bf16_not_finite(y)) o[d] += __uint_as_float(y << 16);
+        }
+      }
+    }
+  }
+}
+
+template <bool DUALK, int LAYOUT>
+__device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, int warp, int lane,
+                          const WaitCtl wc) {
+  using Cfg = AtCfg<DUALK>;
+  constexpr int ST = Cfg::ST;
+  const int t = warp >> 2, w = warp & 3, r = w * 32 + lane;
+  const uint32_t lanes = (uint32_t)(32 * w) << 16;
+  const uint32_t ts = tmem + lanes + kColS + 128u * t, to = tmem + lanes + kColO + 128u * t;
+  const float qs = p.qscale;
+  int sc = 0, oc[2] = {0, 0}, base = 0;
+  for (int it = 0;; ++it) {
+    if (!warp_wait(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc, lane)) return;
+    const Item x = sm.item[it & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.it_empty[it & 1]);
+    if (x.kb1 < 0) return;
+    const int n = x.kb1 - x.kb0, mine = DUALK ? (n - t + 1) / 2 : n;
+    const int first_tok = x.tok0 + (DUALK ? 0 : t * (kRows >> p.g_log2));
+    const int tok = first_tok + (r >> p.g_log2);
+    const bool idle = first_tok + ((w * 32) >> p.g_log2) >= x.T;  // no row of this warp is one of the sequence
+    float m = -INFINITY, l = 0.f;
+    for (int jj = 0; jj < mine; ++jj) {
+      const int j = DUALK ? 2 * jj + t : jj, k0 = (x.kb0 + j) * kBN;
+      const bool masked = block_masked(p, x, k0);
+      if (masked) {
+        const int vi = base + (DUALK ? min(n, j + 2) + j : 2 * j + 1);  // the load that brought V
+        if (!warp_wait(&sm.kv_full[vi % ST], (uint32_t)((vi / ST) & 1), wc, lane)) return;
+        if (clean_v(sm.kv[vi % ST], r, &sm.poison[it & 1], it + 1))
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      if (!warp_wait(&sm.s_full[t], (uint32_t)(sc & 1), wc, lane)) return;
+      ++sc;
+      tc_fence_after();
+      if (!idle) {
+        float s[128];
+        {
+          uint32_t u[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_nowait<32>(ts + 32u * c, u[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(u[c >> 5][c & 31]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t bits = sees(p, x, tok, k0 + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((bits >> e) & 1u)) s[32 * c + e] = -INFINITY;
+          }
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 128; c += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;
+        const bool up = top > m + kSlack;
+        if (__any_sync(kFull, up)) {
+          const float mn = up ? top : m;
+          const float a = up ? ex2(m - mn) : 1.f;
+          m = mn;
+          l *= a;
+          if (jj > 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld_nowait<32>(to + 32u * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              uint32_t h0[16], h1[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                h0[e] = o[e];
+                h1[e] = o[16 + e];
+              }
+              tmem_st<16>(to + 32u * c, h0);
+              tmem_st<16>(to + 32u * c + 16u, h1);
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float &x0 = s[32 * c + e], &x1 = s[32 * c + e + 1];
+            fma2(x0, x1, qs, mu);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            sum[e & 2] += x0;
+            sum[(e & 2) + 1] += x1;
+            pw[e / 2] = pack_bf16(x0, x1);
+          }
+          tmem_st<16>(ts + 16u * c, pw);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[t]);
+    }
+    base += 2 * n;
+
+    // output: O / l, or O, m and l as a partial
+    float f0 = 1.f, f1 = 0.f;  // DUALK: factors of the two halves' O
+    if (DUALK) {
+      sm.ml[t][0][r] = m;
+      sm.ml[t][1][r] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ml_full);
+      if (!warp_wait(&sm.ml_full, (uint32_t)(it & 1), wc, lane)) return;
+      const float m0 = sm.ml[0][0][r], m1 = sm.ml[1][0][r];
+      m = fmaxf(m0, m1);
+      f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
+      f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+      l = sm.ml[0][1][r] * f0 + sm.ml[1][1][r] * f1;
+      for (int i = 0; i < 2 && i < n; ++i, ++oc[i - 1])
+        if (!warp_wait(&sm.o_full[i], (uint32_t)(oc[i] & 1), wc, lane)) return;
+    } else {
+      if (!warp_wait(&sm.o_full[t], (uint32_t)(oc[t] & 1), wc, lane)) return;
+      ++oc[t];
+    }
+    tc_fence_after();
+    if (!idle) {
+      const bool poisoned = sm.poison[it & 1] == it + 1;
+      const bool mine_row = tok < x.T;
+      const float inv = x.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const int row = (DUALK ? 0 : 128 * t) + r;
+      const int64_t orow = (x.row0 + tok) * p.hq + ((int64_t)x.h << p.g_log2) + (r & (p.g - 1));
+      constexpr int kChunks = DUALK ? 2 : 4;  // DUALK: each group takes 64 of the dims
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int d0 = (DUALK ? 64 * t : 0) + 32 * c;
+        const uint32_t col = tmem + lanes + kColO + (DUALK ? 0u : 128u * t) + (uint32_t)d0;
+        float o[32];
+        {
+          uint32_t u[32];
+          tmem_ld_nowait<32>(col, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * (DUALK ? f0 : 1.f);
+          if (DUALK && n > 1) {
+            tmem_ld_nowait<32>(col + 128u, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(u[e]), f1, o[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        if (poisoned) {
+          float y[32];  // a copy, so that o itself stays in registers
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = o[e];
+          add_not_finite<LAYOUT>(p, x, tok, d0, y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = y[e];
+        }
+        if (mine_row) {
+          if (x.slot >= 0) {
+            float4 *dst = reinterpret_cast<float4 *>(p.part_o + ((int64_t)x.slot * Cfg::ROWS + row) * 128 + d0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * 128 + d0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                  pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+          }
+        }
+      }
+      if (mine_row && (!DUALK || t == 0)) {
+        if (x.slot >= 0)
+          *reinterpret_cast<float2 *>(p.part_ml + ((int64_t)x.slot * Cfg::ROWS + row) * 2) = make_float2(m, l);
+        else if (p.lse != nullptr)
+          p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+    }
+    tc_fence_before();
+    if (DUALK) {
+      // the next item's products may overwrite O once both groups have read it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_read);
+      if (!warp_wait(&sm.o_read, (uint32_t)(it & 1), wc, lane)) return;
+    }
+  }
+}
+
+template <bool DUALK, int LAYOUT>
+__global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
+  using Cfg = AtCfg<DUALK>;
+  extern __shared__ uint8_t smem_dyn[];
+  AtSmem<DUALK> &sm = *reinterpret_cast<AtSmem<DUALK> *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::ST; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_empty[i], 1);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.it_full[i], 1);
+      mbar_init(&sm.it_empty[i], kSoftWarps + 1);
+      sm.poison[i] = 0;
+    }
+    mbar_init(&sm.ml_full, kSoftWarps);
+    mbar_init(&sm.o_read, kSoftWarps);
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kIssueWarp) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const WaitCtl wc = wait_ctl(&sm.abort_flag, p.status, 0);
+  if (warp < kSoftWarps) {
+    soft_role<DUALK, LAYOUT>(p, sm, tmem, warp, lane, wc);
+  } else if (warp == kLoadWarp) {
+    if constexpr (LAYOUT == kPacked)
+      load_role<DUALK, LAYOUT, PromptCursor<DUALK>>(p, sm, lane, wc);
+    else
+      load_role<DUALK, LAYOUT, TreeCursor<DUALK, LAYOUT>>(p, sm, lane, wc);
+  } else {
+    if (lane == 0) mma_role<DUALK>(p, sm, tmem, wc);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssueWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Partials of a unit (sequence, KV head, tile of rows) that several CTAs
+// worked on, put together: out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
+// One warp per row, a lane holds 4 dims.
+// ---------------------------------------------------------------------------
+constexpr int kCombineWarps = 8;
+
+template <bool DUALK, int LAYOUT>
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const __grid_constant__ AttendParams p, int grid) {
+  constexpr int ROWS = AtCfg<DUALK>::ROWS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
+  const int tpi = ROWS >> p.g_log2, tok0 = blockIdx.y * tpi;
+  int T, ctx;
+  int64_t row0;
+  bool bad;
+  seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
+  if (tok0 >= T) return;
+  int64_t all = 0, before = 0;  // key blocks of every sequence, of those before s
+  for (int i = lane; i < p.n_seq; i += 32) {
+    int t, c;
+    int64_t r;
+    seq_of<LAYOUT>(p, i, t, c, r, bad);
+    const int64_t n = seq_blocks<ROWS>(p, c, t);
+    all += n;
+    if (i < s) before += n;
+  }
+  all = warp_sum(all);
+  before = warp_sum(before);
+  const int64_t w = (all + grid - 1) / grid;
+  int64_t ub = before + h * (seq_blocks<ROWS>(p, ctx, T) / p.hkv);
+  for (int t = 0; t < tok0; t += tpi) ub += key_blocks(p, ctx, T, t + tpi);
+  const int nb = key_blocks(p, ctx, T, tok0 + tpi);
+  const int c0 = (int)(ub / w), c1 = (int)((ub + nb - 1) / w);
+  if (c0 == c1) return;  // one CTA did it all and wrote the output
+  const int rows = min(T - tok0, tpi) << p.g_log2;
+  for (int r = blockIdx.z * kCombineWarps + warp; r < rows; r += gridDim.z * kCombineWarps) {
+    auto at = [&](int c) { return (int64_t)(2 * c + (c == c0 && ub > c0 * w ? 1 : 0)) * ROWS + r; };
+    float M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.part_ml + at(c) * 2));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c) * 2));
+      const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(c) * 128) + lane);
+      const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      L = fmaf(a, ml.y, L);
+      acc.x = fmaf(a, o.x, acc.x);
+      acc.y = fmaf(a, o.y, acc.y);
+      acc.z = fmaf(a, o.z, acc.z);
+      acc.w = fmaf(a, o.w, acc.w);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t orow = (row0 + tok0 + (r >> p.g_log2)) * p.hq + ((int64_t)h << p.g_log2) + (r & (p.g - 1));
+    *reinterpret_cast<uint2 *>(p.out + orow * 128 + 4 * lane) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (p.lse != nullptr && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool strides_ok(int64_t tok, int64_t head) { return tok > 0 && head > 0 && tok % 8 == 0 && head % 8 == 0; }
@@ -122,18 +992,115 @@ tria_status check_desc(const tria_model_desc &d) {
 // What both operators ask of the queries and the outputs.
 tria_status check_rows(const void *q, int64_t q_tok, int64_t q_head, int64_t n_tokens,
                        const int32_t *starts, float scale, const void *out, const float *lse) {
-  if (n_tokens < 0 || n_tokens > INT32_MAX || !std::isfinite(scale) || !(scale > 0.f)) return TRIA_ERR_INVALID_ARG;
+  if (n_tokens < 0 || n_tokens > INT32_MAX - 1024 || !std::isfinite(scale) || !(scale > 0.f)) return TRIA_ERR_INVALID_ARG;
   if (!strides_ok(q_tok, q_head) || starts == nullptr || !aligned(starts, 4)) return TRIA_ERR_INVALID_ARG;
   if (n_tokens > 0 && (q == nullptr || out == nullptr)) return TRIA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return TRIA_ERR_INVALID_ARG;
   return TRIA_OK;
 }
 
-tria_status launch_attend(const AttendParams &p, int64_t max_tokens, cudaStream_t st) {
-  int64_t x = (max_tokens + kWarps - 1) / kWarps;
-  if (x > 2048) x = 2048;
-  attend_kernel<<<dim3((unsigned)x, (unsigned)p.n_seq, (unsigned)p.hq), 32 * kWarps, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+void fill_rows(AttendParams &p, const tria_model_desc &d, int n_seq, int64_t n_tokens, const int32_t *starts,
+               float scale, void *out, float *lse, void *ws) {
+  p.n_seq = n_seq;
+  p.hq = d.n_q_heads;
+  p.hkv = d.n_kv_heads;
+  p.g = p.hq / p.hkv;
+  for (p.g_log2 = 0; (1 << p.g_log2) < p.g; ++p.g_log2) {}
+  p.n_tokens = n_tokens;
+  p.starts = starts;
+  p.qscale = (float)((double)scale * 1.4426950408889634);
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  p.status = reinterpret_cast<int32_t *>(static_cast<unsigned char *>(ws) + 4);
+}
+
+// q as tiles of 128 rows: 128 / G tokens x the G heads of a KV head x 64 dims
+bool query_map(CUtensorMap *map, const void *q, int64_t tok, int64_t head, int hq, int g, int64_t n_tokens) {
+  const uint64_t dims[4] = {128, (uint64_t)hq, (uint64_t)n_tokens, 1};
+  const int64_t strides[3] = {head, tok, 0};
+  const uint32_t box[4] = {64, (uint32_t)g, (uint32_t)(kRows / g), 1};
+  return encode_rows_map(map, q, dims, strides, box);
+}
+
+bool cache_map(CUtensorMap *map, const void *base, const RowsView &v) {
+  if (v.layout == TRIA_LAYOUT_CONTIGUOUS) {
+    const uint64_t dims[4] = {128, (uint64_t)v.max_seq_len, (uint64_t)v.hkv, (uint64_t)v.n_seq};
+    const int64_t strides[3] = {v.s_tok, v.s_head, v.s_seq};
+    const uint32_t box[4] = {64, (uint32_t)kBN, 1, 1};
+    return encode_rows_map(map, base, dims, strides, box);
+  }
+  const uint64_t dims[4] = {128, (uint64_t)v.hkv, (uint64_t)v.block_size, (uint64_t)v.num_blocks};
+  const int64_t strides[3] = {v.s_head, v.s_tok, v.s_blk};
+  const uint32_t box[4] = {64, 1, (uint32_t)v.block_size, 1};
+  return encode_rows_map(map, base, dims, strides, box);
+}
+
+bool packed_map(CUtensorMap *map, const void *base, int64_t tok, int64_t head, int hkv, int64_t n_tokens) {
+  const uint64_t dims[4] = {128, (uint64_t)n_tokens, (uint64_t)hkv, 1};
+  const int64_t strides[3] = {tok, head, 0};
+  const uint32_t box[4] = {64, (uint32_t)kBN, 1, 1};
+  return encode_rows_map(map, base, dims, strides, box);
+}
+
+cudaError_t sm_count(int *sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+template <bool DUALK, int LAYOUT>
+cudaError_t launch_attend(const AttendParams &p, int grid, cudaStream_t st) {
+  const int smem = (int)sizeof(AtSmem<DUALK>) + 1024;
+  static_assert(sizeof(AtSmem<DUALK>) + 1024 <= kMaxDynSmem, "shared memory of the attention kernel");
+  // the shared-memory opt-in once per device (it is a property of the kernel)
+  static thread_local int attr_dev = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (attr_dev != dev) {
+    e = cudaFuncSetAttribute(attend_kernel<DUALK, LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_dev = dev;
+  }
+  attend_kernel<DUALK, LAYOUT><<<grid, kAtThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+// Tiles of rows per (sequence, KV head) at most, and rows of a partial.
+struct TreeShape {
+  bool dualk;
+  int rows, tiles, grid;
+};
+
+tria_status tree_shape(const tria_model_desc &d, const tria_cache_view *c, int max_draft, TreeShape *sh) {
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) return TRIA_ERR_CUDA;
+  const int g = d.n_q_heads / d.n_kv_heads;
+  // up to 128 rows fit one tile
+  sh->dualk = (int64_t)max_draft * g <= kRows;
+  sh->rows = sh->dualk ? AtCfg<true>::ROWS : AtCfg<false>::ROWS;
+  sh->tiles = (int)(((int64_t)max_draft * g + sh->rows - 1) / sh->rows);
+  const int64_t blocks = (int64_t)c->n_seq * d.n_kv_heads * sh->tiles * ((c->max_seq_len + (int64_t)kBN - 1) / kBN);
+  sh->grid = blocks < sms ? (int)blocks : sms;
+  return TRIA_OK;
+}
+
+size_t tree_ws_bytes(const TreeShape &sh) {
+  return kHeaderBytes + (size_t)2 * sh.grid * sh.rows * (128 + 2) * sizeof(float);
+}
+
+template <bool DUALK, int LAYOUT>
+cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t st) {
+  const cudaError_t e = launch_attend<DUALK, LAYOUT>(p, sh.grid, st);
+  if (e != cudaSuccess || sh.grid == 1) return e;
+  // about two blocks per SM over all units, as far as there are rows for their warps
+  const int64_t units = (int64_t)p.n_seq * p.hkv * sh.tiles;
+  const int64_t rows = (int64_t)p.max_draft * p.g < sh.rows ? (int64_t)p.max_draft * p.g : sh.rows;
+  int64_t z = (2 * 148 + units - 1) / units;
+  if (z > (rows + kCombineWarps - 1) / kCombineWarps) z = (rows + kCombineWarps - 1) / kCombineWarps;
+  const dim3 grid((unsigned)(p.n_seq * p.hkv), (unsigned)sh.tiles, (unsigned)z);
+  combine_kernel<DUALK, LAYOUT><<<grid, 32 * kCombineWarps, 0, st>>>(p, sh.grid);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -165,26 +1132,21 @@ tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q, in
   if ((st = check_header_workspace(ws, ws_bytes, kHeaderBytes)) != TRIA_OK) return st;
   if (n_tokens == 0) return TRIA_OK;
   AttendParams p{};
-  p.q = static_cast<const uint16_t *>(q);
-  p.k = static_cast<const uint16_t *>(k);
+  fill_rows(p, *desc, n_seq, n_tokens, starts, scale, out, lse, ws);
   p.v = static_cast<const uint16_t *>(v);
-  p.q_tok = q_tok;
-  p.q_head = q_head;
-  p.k_tok = k_tok;
-  p.k_head = k_head;
   p.v_tok = v_tok;
   p.v_head = v_head;
-  p.starts = starts;
-  p.n_seq = n_seq;
-  p.hq = desc->n_q_heads;
-  p.hkv = desc->n_kv_heads;
-  p.g = p.hq / p.hkv;
-  p.n_tokens = n_tokens;
-  p.scale = scale;
-  p.out = static_cast<uint16_t *>(out);
-  p.lse = lse;
-  p.status = reinterpret_cast<int32_t *>(static_cast<unsigned char *>(ws) + 4);
-  return launch_attend(p, n_tokens, reinterpret_cast<cudaStream_t>(stream));
+  if (!query_map(&p.qmap, q, q_tok, q_head, p.hq, p.g, n_tokens) ||
+      !packed_map(&p.kmap, k, k_tok, k_head, p.hkv, n_tokens) ||
+      !packed_map(&p.vmap, v, v_tok, v_head, p.hkv, n_tokens))
+    return TRIA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) return TRIA_ERR_CUDA;
+  // at most one item per tile of rows and KV head, the sequences' last tiles part full
+  const int64_t tiles = (n_tokens * p.g + AtCfg<false>::ROWS - 1) / AtCfg<false>::ROWS + n_seq;
+  const int grid = (int)(tiles * p.hkv < sms ? tiles * p.hkv : sms);
+  const cudaError_t e = launch_attend<false, kPacked>(p, grid, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
 
 tria_status tria_tree_workspace_size(const tria_stats *stats, const tria_cache_view *cache, int max_draft,
@@ -192,7 +1154,12 @@ tria_status tria_tree_workspace_size(const tria_stats *stats, const tria_cache_v
   if (stats == nullptr || cache == nullptr || bytes == nullptr) return TRIA_ERR_INVALID_ARG;
   if (cache->n_seq < 1 || cache->n_seq > TRIA_MAX_SEQS || max_draft < 1 || max_draft > cache->max_seq_len)
     return TRIA_ERR_INVALID_ARG;
-  *bytes = kHeaderBytes;
+  tria_model_desc d;
+  tria_status st = tria_stats_desc(stats, &d);
+  if (st != TRIA_OK || (st = check_desc(d)) != TRIA_OK) return st;
+  TreeShape sh;
+  if ((st = tree_shape(d, cache, max_draft, &sh)) != TRIA_OK) return st;
+  *bytes = tree_ws_bytes(sh);
   return TRIA_OK;
 }
 
@@ -209,29 +1176,29 @@ tria_status tria_tree_attention(const tria_stats *stats, const tria_cache_view *
   if ((st = check_rows(q, q_tok, q_head, n_tokens, starts, scale, out, lse)) != TRIA_OK) return st;
   if (max_draft < 1 || max_draft > cache->max_seq_len) return TRIA_ERR_INVALID_ARG;
   if (mask != nullptr && (!aligned(mask, 4) || mask_words < (max_draft + 31) / 32)) return TRIA_ERR_INVALID_ARG;
-  if ((st = check_header_workspace(ws, ws_bytes, kHeaderBytes)) != TRIA_OK) return st;
+  TreeShape sh;
+  if ((st = tree_shape(d, cache, max_draft, &sh)) != TRIA_OK) return st;
+  if ((st = check_header_workspace(ws, ws_bytes, tree_ws_bytes(sh))) != TRIA_OK) return st;
   if (n_tokens == 0) return TRIA_OK;
-  p.q = static_cast<const uint16_t *>(q);
-  p.k = static_cast<const uint16_t *>(cache->k_layers[layer]);
+  fill_rows(p, d, cache->n_seq, n_tokens, starts, scale, out, lse, ws);
   p.v = static_cast<const uint16_t *>(cache->v_layers[layer]);
-  p.q_tok = q_tok;
-  p.q_head = q_head;
   p.layer = layer;
-  p.cached = 1;
-  p.starts = starts;
-  p.n_seq = cache->n_seq;
-  p.hq = d.n_q_heads;
-  p.hkv = d.n_kv_heads;
-  p.g = p.hq / p.hkv;
-  p.n_tokens = n_tokens;
   p.max_draft = max_draft;
   p.mask = mask;
   p.mask_words = mask_words;
-  p.scale = scale;
-  p.out = static_cast<uint16_t *>(out);
-  p.lse = lse;
-  p.status = reinterpret_cast<int32_t *>(static_cast<unsigned char *>(ws) + 4);
-  return launch_attend(p, max_draft, reinterpret_cast<cudaStream_t>(stream));
+  p.part_o = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
+  p.part_ml = p.part_o + (size_t)2 * sh.grid * sh.rows * 128;
+  if (!query_map(&p.qmap, q, q_tok, q_head, p.hq, p.g, n_tokens) ||
+      !cache_map(&p.kmap, cache->k_layers[layer], p.view) || !cache_map(&p.vmap, cache->v_layers[layer], p.view))
+    return TRIA_ERR_UNSUPPORTED;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (p.view.layout == TRIA_LAYOUT_PAGED)
+    e = sh.dualk ? launch_tree<true, TRIA_LAYOUT_PAGED>(p, sh, cs) : launch_tree<false, TRIA_LAYOUT_PAGED>(p, sh, cs);
+  else
+    e = sh.dualk ? launch_tree<true, TRIA_LAYOUT_CONTIGUOUS>(p, sh, cs)
+                 : launch_tree<false, TRIA_LAYOUT_CONTIGUOUS>(p, sh, cs);
+  return e == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
 
 }  // extern "C"

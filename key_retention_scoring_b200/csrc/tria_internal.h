@@ -232,6 +232,11 @@ tria_status make_rows_view(const tria_stats *stats, const tria_cache_view *cache
                            int layer1, tria_model_desc *desc, RowsView *view);
 tria_status check_header_workspace(void *ws, size_t have, size_t need);
 
+// Tensor map of bf16 rows: dims innermost first, strides in elements of
+// dimensions 1 .. 3, 128-byte swizzle, zero fill outside (tria_api.cu).
+bool encode_rows_map(CUtensorMap *map, const void *base, const uint64_t (&dims)[4],
+                     const int64_t (&strides)[3], const uint32_t (&box)[4]);
+
 constexpr size_t kHeaderBytes = 256;  // workspace header; status flags at byte 4
 
 // N of (s, layer), or -1 when it lies outside [0, max_seq_len]
