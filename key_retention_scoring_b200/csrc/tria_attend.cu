@@ -18,7 +18,7 @@
 //   warps 0-3, 4-7  softmax of tile (or half) 0 and 1, one thread per row:
 //                   S from tensor memory, running maximum and sum in fp32,
 //                   P as bf16 back over S, the output at the end;
-//   warp 8          one lane issues tcgen05.mma: S = Q K^T (both in shared
+//   warp 8          issues tcgen05.mma (one elected lane): S = Q K^T (both in shared
 //                   memory), O += P V (P in tensor memory, V as it lies,
 //                   MN-major); while one tile's softmax runs, the other's
 //                   products do;
@@ -35,6 +35,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -49,11 +50,45 @@ namespace {
 using namespace dev;
 using namespace tc;
 
-constexpr int kBN = 128;                       // keys per block
+// Waits of the pipeline: the threads sleep in the barrier unit, at most hint_ns
+// at a time; the timer and the abort flag are looked at after a sleep that ran
+// out.
+__device__ __forceinline__ bool poll_on(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+  const uint64_t t0 = global_timer();
+  for (;;) {
+    if (mbar_try_sleep(bar, parity, w.hint_ns)) return true;
+    if (*w.abort_flag) return false;
+    if (global_timer() - t0 > w.limit_ns) {
+      flag_expiry(w);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_sleep(a, parity, w.hint_ns) || poll_on(a, parity, w);
+}
+
+// The same for a whole warp, which leaves together.
+__device__ __forceinline__ bool warp_poll(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
+  const uint32_t a = smem_u32(bar);
+  if (__all_sync(kFull, mbar_try_sleep(a, parity, w.hint_ns))) return true;
+  return __all_sync(kFull, poll_on(a, parity, w));
+}
+
+constexpr int kBN = 128;                       // keys per block (a ring stage of K or V)
+constexpr int kHN = 64;                        // keys per step (a product and its softmax)
+constexpr int kNB = kBN / kHN;                 // steps per block, and buffers of S in tensor memory
 constexpr int kTile = 2 * kHalfBlock;          // bytes of 128 rows x 128 bf16
 constexpr int kSoftWarps = 8;
-constexpr int kIssueWarp = 8, kLoadWarp = 9;
-constexpr int kAtThreads = 320;
+constexpr int kIssueWarp = 8, kLoadWarp = 9;   // issue: 8 and 10
+constexpr int kAtThreads = 384;                 // the third warpgroup holds the two single-warp roles
+// Registers a thread: the kernel is launched with 168 (65536 / 384, rounded
+// down to 8); the softmax groups hold a row of S and raise theirs, the third
+// group gives up what they take (2 x 208 + 88 = 3 x 168).
+constexpr int kLaunchRegs = 168, kSoftRegs = 208, kRoleRegs = 88;
+static_assert(2 * kSoftRegs + kRoleRegs == 3 * kLaunchRegs, "register split");
 constexpr int kPacked = 2;                     // LAYOUT of prompts, next to the cache layouts
 constexpr uint32_t kColS = 0, kColO = 256;     // tensor-memory columns: S (and P) of half t at 128 t, O after them
 constexpr float kLn2 = 0.6931471805599453f;
@@ -61,6 +96,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // more than this, so most blocks leave O in tensor memory alone; weights stay
 // below 2^8, well inside fp32 and bf16.
 constexpr float kSlack = 8.f;
+// Of every 8 pairs of exponentials this many run on the FMA pipe, the rest on the
+// special-function unit.
+constexpr int kFmaOf8 = 1;
 
 struct AttendParams {
   CUtensorMap qmap, kmap, vmap;
@@ -83,6 +121,7 @@ struct AttendParams {
 // One piece of work: rows of tokens [tok0, ..) of (s, h) against key blocks [kb0, kb1).
 struct Item {
   int s, h, tok0, T, ctx, kb0, kb1, slot;      // slot: -1 writes the output, else a partial
+  int halves;                                  // half blocks with keys that some row sees
   int64_t row0;                                // first row of the sequence in q and out
 };
 
@@ -98,7 +137,7 @@ struct AtSmem {
   alignas(1024) uint8_t q[AtCfg<DUALK>::QT][kTile];
   alignas(1024) uint8_t kv[AtCfg<DUALK>::ST][kTile];
   alignas(8) uint64_t kv_full[AtCfg<DUALK>::ST], kv_empty[AtCfg<DUALK>::ST];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], it_full[2], it_empty[2], ml_full, o_read, drain;
+  uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_done[2], o_full[2], it_full[2], it_empty[2], ml_full, o_read, drain[2];
   Item item[2];
   float ml[DUALK ? 2 : 1][2][DUALK ? 128 : 1];
   volatile int poison[2];
@@ -130,6 +169,29 @@ __device__ __forceinline__ void seq_of(const AttendParams &p, int s, int &T, int
 __device__ __forceinline__ int key_blocks(const AttendParams &p, int ctx, int T, int tok_end) {
   const int n = ctx + (p.mask != nullptr ? T : min(T, tok_end));
   return (n + kBN - 1) / kBN;
+}
+
+// half blocks of a piece [kb0, kb1) that hold a key some row sees
+__device__ __forceinline__ int half_blocks(const AttendParams &p, const Item &x, int tok_end) {
+  const int keys = x.ctx + (p.mask != nullptr ? x.T : min(x.T, tok_end));
+  return min(kNB * (x.kb1 - x.kb0), (keys - x.kb0 * kBN + kHN - 1) / kHN);
+}
+
+// Halves of a piece that half t of the CTA works on, and where the ring's loads
+// hold K and V of block j (the order in which mma_role uses them).
+template <bool DUALK>
+__device__ __forceinline__ int halves_of(int n, int halves, int t) {
+  if (!DUALK) return halves;
+  const int blocks = (n - t + 1) / 2;
+  return kNB * blocks - (((n - 1) & 1) == t ? kNB * n - halves : 0);
+}
+template <bool DUALK>
+__device__ __forceinline__ int k_load(int n, int j) {
+  return DUALK ? (j < 2 ? j : 2 * j - 1) : 2 * j;
+}
+template <bool DUALK>
+__device__ __forceinline__ int v_load(int n, int j) {
+  return DUALK ? min(n, j + 2) + j : 2 * j + 1;
 }
 
 // key blocks of all (KV head, tile of ROWS rows) units of a sequence
@@ -226,6 +288,7 @@ struct PromptCursor {
     x.tok0 = lo * tpi(p);
     x.kb0 = 0;
     x.kb1 = key_blocks(p, 0, x.T, x.tok0 + tpi(p));
+    x.halves = half_blocks(p, x, x.tok0 + tpi(p));
     x.slot = -1;
     return true;
   }
@@ -323,6 +386,7 @@ struct TreeCursor {
     x.row0 = row0;
     x.kb0 = (int)(pos - ub);
     x.kb1 = (int)(min(end, ub + nb) - ub);
+    x.halves = half_blocks(p, x, tok0 + tpi(p));
     x.slot = x.kb1 - x.kb0 == nb ? -1 : 2 * (int)blockIdx.x + (pieces > 0 ? 1 : 0);
     pos = ub + x.kb1;
     ++pieces;
@@ -354,7 +418,7 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
   Item x{};
   auto wait = [&](uint64_t *bar, int phase) {
     bool good = true;
-    if (lane == 0) good = mbar_wait(bar, (uint32_t)(phase & 1), wc);
+    if (lane == 0) good = poll(bar, (uint32_t)(phase & 1), wc);
     return __shfl_sync(kFull, good ? 1 : 0, 0) != 0;
   };
   int next_blk = -1, next_j = -1;
@@ -436,7 +500,7 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
 }
 
 // ---------------------------------------------------------------------------
-// products (one lane)
+// products
 // ---------------------------------------------------------------------------
 // V tile as the B operand of O += P V: N = dims, which lie contiguous (MN-
 // major): 128-byte swizzle, the two 64-dim halves kHalfBlock bytes apart
@@ -450,107 +514,106 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
   return d;
 }
 
-constexpr uint32_t kIdescS = idesc_bf16_m128_n(kBN);
+constexpr uint32_t kIdescS = idesc_bf16_m128_n(kHN);
 constexpr uint32_t kIdescO = idesc_bf16_m128_n(kHeadDim) | (1u << 16);  // B is MN-major
 
+// The products are issued by one elected lane of a warp that stays together,
+// several to one asm block: an issue from a diverged lane took 64 cycles
+// whatever the product's size (the operands went through the vector registers
+// one by one), one of these takes 20, and a step of 16 keys takes 64.
+#define TRIA_MMA_QK(step) \
+  "add.s64 x, %1, " step ";\n add.s64 y, %2, " step ";\n" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n"
+// S = Q K^T: 8 steps of 16 dims; a step is 32 bytes on in the swizzled rows,
+// four steps on is the other 64-dim half.
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  static_assert(kHalfBlock >> 4 == 1024, "descriptor offset of the second half");
+  asm volatile(
+      "{\n .reg .pred q, t, f;\n .reg .b64 x, y;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 t, 1, 0;\n"
+      " setp.ne.b32 f, 0, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+      TRIA_MMA_QK("2") TRIA_MMA_QK("4") TRIA_MMA_QK("6") TRIA_MMA_QK("1024") TRIA_MMA_QK("1026")
+      TRIA_MMA_QK("1028") TRIA_MMA_QK("1030") "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+#undef TRIA_MMA_QK
+
+#define TRIA_MMA_PV(col, row) \
+  "add.s32 z, %1, " col ";\n add.s64 y, %2, " row ";\n" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n"
+// O += P V: 4 steps of 16 keys, 8 columns of P and 16 rows of V each.
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred q, t, f;\n .reg .b64 y;\n .reg .b32 z;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 t, 1, 0;\n"
+      " setp.ne.b32 f, %4, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n"
+      TRIA_MMA_PV("8", "128") TRIA_MMA_PV("16", "256") TRIA_MMA_PV("24", "384")
+      "}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+#undef TRIA_MMA_PV
+
+__device__ __forceinline__ void elect_commit(uint64_t *bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+// One warp for each half t of the CTA: the tensor core takes their products in
+// turn, and neither waits where the other waits for its softmax.
 template <bool DUALK>
-__device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, const WaitCtl wc) {
+__device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, int t, int lane, const WaitCtl wc) {
   using Cfg = AtCfg<DUALK>;
   constexpr int ST = Cfg::ST;
-  int li = 0, pc[2] = {0, 0};
+  constexpr uint32_t kHalfRows = (kHN * 128) >> 4;  // 64 rows on in a tile, as a descriptor offset
+  const uint32_t s_col = tmem + kColS + 128u * t, o_col = tmem + kColO + 128u * t;
+  const uint64_t q_at = sw128_desc(smem_u32(&sm.q[DUALK ? 0 : t][0]));
+  const uint64_t k_at = sw128_desc(smem_u32(&sm.kv[0][0])), v_at = v_desc(smem_u32(&sm.kv[0][0]));
+  int base = 0;
+  uint32_t pp = 0;  // phases of p_full, bit b
   bool ok = true, issued = false;
-  auto kv_wait = [&](int i) { return mbar_wait(&sm.kv_full[i % ST], (uint32_t)((i / ST) & 1), wc); };
-  auto qk = [&](int t, int i) {
-    const uint64_t a = sw128_desc(smem_u32(&sm.q[DUALK ? 0 : t][0])), b = sw128_desc(smem_u32(&sm.kv[i % ST][0]));
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const uint32_t o = (uint32_t)((s >> 2) * kHalfBlock + (s & 3) * 32) >> 4;
-      mma_bf16(tmem + kColS + 128u * t, a + o, b + o, kIdescS, s > 0 ? 1u : 0u);
-    }
-    issued = true;
-  };
-  auto pv = [&](int t, int i, bool first) {
-    const uint64_t b = v_desc(smem_u32(&sm.kv[i % ST][0]));
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-      mma_bf16_ta(tmem + kColO + 128u * t, tmem + kColS + 128u * t + 8u * s, b + (uint64_t)((s * 2048) >> 4), kIdescO,
-                  first && s == 0 ? 0u : 1u);
-  };
-  auto p_wait = [&](int t) {
-    const bool good = mbar_wait(&sm.p_full[t], (uint32_t)(pc[t] & 1), wc);
-    ++pc[t];
-    tc_fence_after();
-    return good;
-  };
   for (int it = 0; ok; ++it) {
-    if (!(ok = mbar_wait(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc))) break;
-    const int n = sm.item[it & 1].kb1 - sm.item[it & 1].kb0;
+    if (!(ok = warp_poll(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc))) break;
+    const int n = sm.item[it & 1].kb1 - sm.item[it & 1].kb0, halves = sm.item[it & 1].halves;
     const bool end = sm.item[it & 1].kb1 < 0;
-    mbar_arrive(&sm.it_empty[it & 1]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.it_empty[it & 1]);
     if (end) break;
-    if (!(ok = mbar_wait(&sm.q_full, (uint32_t)(it & 1), wc))) break;
-    if (DUALK) {
-      for (int t = 0; t < 2 && t < n; ++t) {
-        if (!(ok = kv_wait(li))) break;
-        tc_fence_after();
-        qk(t, li);
-        mma_commit(&sm.kv_empty[li % ST]);
-        mma_commit(&sm.s_full[t]);
-        ++li;
-      }
-      if (ok && n <= 2) mma_commit(&sm.q_empty);
-      for (int j = 0; ok && j < n; ++j) {
-        const int t = j & 1;
-        if (!(ok = kv_wait(li) && p_wait(t))) break;
-        pv(t, li, j < 2);
-        mma_commit(&sm.kv_empty[li % ST]);
-        ++li;
-        if (j + 2 < n) {
-          if (!(ok = kv_wait(li))) break;
-          qk(t, li);
-          mma_commit(&sm.kv_empty[li % ST]);
-          mma_commit(&sm.s_full[t]);
-          ++li;
-          if (j + 3 == n) mma_commit(&sm.q_empty);
-        } else {
-          mma_commit(&sm.o_full[t]);
-        }
-      }
-    } else {
-      if (!(ok = kv_wait(li))) break;
+    if (!(ok = warp_poll(&sm.q_full, (uint32_t)(it & 1), wc))) break;
+    const int mine = halves_of<DUALK>(n, halves, t);
+    if (mine == 0 && lane == 0) mbar_arrive(&sm.q_empty);
+    auto kv_wait = [&](int i) { return warp_poll(&sm.kv_full[i % ST], (uint32_t)((i / ST) & 1), wc); };
+    // S of half block g into buffer g & 1; its last half releases K
+    auto qk = [&](int g) {
+      const int i = base + k_load<DUALK>(n, DUALK ? 2 * (g / kNB) + t : g / kNB), b = g % kNB;
+      if (b == 0 && !kv_wait(i)) return false;
+      mma_qk(s_col + 64u * b, q_at, k_at + (uint32_t)((i % ST) * (kTile >> 4)) + b * kHalfRows, kIdescS);
+      elect_commit(&sm.s_full[t][b]);
+      if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[i % ST]);
+      if (g + 1 == mine) elect_commit(&sm.q_empty);
+      issued = true;
+      return true;
+    };
+    for (int g = 0; ok && g < kNB && g < mine; ++g) ok = qk(g);
+    for (int g = 0; ok && g < mine; ++g) {
+      const int b = g % kNB, i = base + v_load<DUALK>(n, DUALK ? 2 * (g / kNB) + t : g / kNB);
+      if (b == 0 && !(ok = kv_wait(i))) break;
+      if (!(ok = warp_poll(&sm.p_full[t][b], (pp >> b) & 1u, wc))) break;
+      pp ^= 1u << b;
       tc_fence_after();
-      for (int t = 0; t < 2; ++t) {
-        qk(t, li);
-        mma_commit(&sm.s_full[t]);
-      }
-      mma_commit(&sm.kv_empty[li % ST]);
-      ++li;
-      if (n == 1) mma_commit(&sm.q_empty);
-      for (int j = 0; ok && j < n; ++j) {
-        const int vi = li, ki = li + 1;
-        if (!(ok = kv_wait(vi))) break;
-        for (int t = 0; t < 2; ++t) {
-          if (!(ok = p_wait(t))) break;
-          pv(t, vi, j == 0);
-          if (t == 1) mma_commit(&sm.kv_empty[vi % ST]);
-          if (j + 1 < n) {
-            if (t == 0 && !(ok = kv_wait(ki))) break;
-            qk(t, ki);
-            mma_commit(&sm.s_full[t]);
-            if (t == 1) mma_commit(&sm.kv_empty[ki % ST]);
-          } else {
-            mma_commit(&sm.o_full[t]);
-          }
-        }
-        li += j + 1 < n ? 2 : 1;
-        if (j + 2 == n) mma_commit(&sm.q_empty);
-      }
+      mma_pv(o_col, s_col + 64u * b, v_at + (uint32_t)((i % ST) * (kTile >> 4)) + b * kHalfRows, kIdescO, g > 0 ? 1u : 0u);
+      if (kNB > 1) elect_commit(&sm.o_done[t]);
+      if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[i % ST]);
+      if (g + 1 == mine) elect_commit(&sm.o_full[t]);
+      if (g + kNB < mine) ok = qk(g + kNB);
     }
+    base += 2 * n;
   }
   // the products already issued must land before the tensor memory is freed
   if (issued) {
-    mma_commit(&sm.drain);
-    mbar_drain(&sm.drain, 0, wc.status);
+    elect_commit(&sm.drain[t]);
+    if (lane == 0) mbar_drain(&sm.drain[t], 0, wc.status);
+    __syncwarp();
   }
 }
 
@@ -563,12 +626,48 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// (a0, a1) * b + c on both halves
-__device__ __forceinline__ void fma2(float &a0, float &a1, float b, float c) {
-  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %3};\n"
-      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b), "f"(c));
+// Two fp32 in a register pair: the packed multiply-add and add take one issue
+// slot for both, and pairs that stay pairs need no moves.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of both on the FMA pipe (far below -126 gives about 2^-126): 2^x = 2^n 2^f
+// with n the nearest integer (the low bits of x + 1.5 2^23) and f in [-1/2,
+// 1/2], 2^f by a polynomial of degree 4 fitted to the smallest maximal relative
+// error (2.7e-6), n added to the exponent bits.
+__device__ __forceinline__ f32x2 exp2_fma(f32x2 v) {
+  float2 x = both(v);
+  v = pair(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+  auto c2 = [](float c) { return pair(c, c); };
+  const f32x2 t = add2(v, c2(12582912.f));
+  const f32x2 f = fma2(add2(t, c2(-12582912.f)), c2(-1.f), v);
+  f32x2 q = fma2(c2(0.009570101276040077f), f, c2(0.05591786280274391f));
+  q = fma2(q, f, c2(0.240247443318367f));
+  q = fma2(q, f, c2(0.6931217908859253f));
+  q = fma2(q, f, c2(0.9999992847442627f));
+  const float2 n = both(t), y = both(q);
+  return pair(__int_as_float(__float_as_int(y.x) + (__float_as_int(n.x) << 23)),
+              __int_as_float(__float_as_int(y.y) + (__float_as_int(n.y) << 23)));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
@@ -578,22 +677,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
 
 __device__ __forceinline__ bool bf16_not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
 
-// Replaces what is not finite in the V tile by 0 (the 128 threads of a softmax
-// group); true where this thread found something.  x * 0 + acc keeps a NaN, so
-// one bf16x2 multiply-add per two values tells whether to look closer.
-__device__ __forceinline__ bool clean_v(uint8_t *tile, int tid, volatile int *poison, int mark) {
+// Replaces what is not finite in half a V tile (64 keys) by 0 (the 128 threads
+// of a softmax group); true where this thread found something.  x * 0 + acc
+// keeps a NaN, so one bf16x2 multiply-add per two values tells whether to look
+// closer.
+__device__ __forceinline__ bool clean_v(uint8_t *half, int tid, volatile int *poison, int mark) {
+  constexpr int kPasses = kHN * 8 / 128;  // of 128 x 16 bytes over the keys of one 64-dim half
+  auto at = [&](int i) { return half + (i / kPasses) * kHalfBlock + ((i % kPasses) * 128 + tid) * 16; };
   uint32_t acc = 0;
 #pragma unroll
-  for (int i = 0; i < kTile / 16 / 128; ++i) {
-    const uint4 w = lds128(tile + (i * 128 + tid) * 16);
+  for (int i = 0; i < 2 * kPasses; ++i) {
+    const uint4 w = lds128(at(i));
     for (uint32_t x : {w.x, w.y, w.z, w.w})
       asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
   }
   if ((acc & 0x7fff7fffu) == 0) return false;
   *poison = mark;
   __threadfence_block();
-  for (int i = 0; i < kTile / 16 / 128; ++i) {
-    uint32_t *w = reinterpret_cast<uint32_t *>(tile + (i * 128 + tid) * 16);
+  for (int i = 0; i < 2 * kPasses; ++i) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(at(i));
     for (int e = 0; e < 4; ++e) {
       const uint32_t x = w[e];
       const uint32_t y = (bf16_not_finite(x) ? 0u : x & 0xffffu) | (bf16_not_finite(x >> 16) ? 0u : x & 0xffff0000u);
@@ -628,18 +730,18 @@ __device__ __forceinline__ uint32_t sees(const AttendParams &p, const Item &x, i
   return bits;
 }
 
-// First key of the item's blocks that hold masked places.
-__device__ __forceinline__ bool block_masked(const AttendParams &p, const Item &x, int k0) {
-  return p.mask != nullptr ? k0 + kBN > x.ctx : k0 + kBN - 1 > x.ctx + x.tok0;
+// Whether the half block of keys from k0 on holds masked places.
+__device__ __forceinline__ bool half_masked(const AttendParams &p, const Item &x, int k0) {
+  return p.mask != nullptr ? k0 + kHN > x.ctx : k0 + kHN - 1 > x.ctx + x.tok0;
 }
 
-// v_j that are not finite, of the masked blocks' keys that this row sees, added to o (dims d0 .. d0 + 31).
+// v_j that are not finite, of the masked half blocks' keys that this row sees, added to o (dims d0 .. d0 + 31).
 template <int LAYOUT>
 __device__ __noinline__ void add_not_finite(const AttendParams &p, const Item &x, int tok, int d0, float (&o)[32]) {
   if (tok >= x.T) return;
-  for (int kb = x.kb0; kb < x.kb1; ++kb) {
-    if (!block_masked(p, x, kb * kBN)) continue;
-    for (int k0 = kb * kBN; k0 < kb * kBN + kBN; k0 += 32) {
+  for (int h0 = x.kb0 * kBN; h0 < x.kb0 * kBN + x.halves * kHN; h0 += kHN) {
+    if (!half_masked(p, x, h0)) continue;
+    for (int k0 = h0; k0 < h0 + kHN; k0 += 32) {
       uint32_t bits = sees(p, x, tok, k0);
       while (bits) {
         const int j = k0 + __ffs(bits) - 1;
@@ -662,6 +764,30 @@ __device__ __noinline__ void add_not_finite(const AttendParams &p, const Item &x
   }
 }
 
+// O *= a for the rows of this warp.  Seldom: kept out of the softmax loop.
+__device__ __noinline__ bool rescale(uint32_t o_col, float a, uint64_t *done, uint32_t parity, const WaitCtl &wc) {
+  // the product before this step's must have been added to O (with one buffer of
+  // S it has: S of this step was issued behind it)
+  if (kNB > 1 && !warp_poll(done, parity, wc)) return false;
+  tc_fence_after();
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    tmem_ld_nowait<32>(o_col + 32u * c, o);
+    tmem_wait_ld();
+    uint32_t o0[16], o1[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      o0[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+      o1[e] = __float_as_uint(__uint_as_float(o[16 + e]) * a);
+    }
+    tmem_st<16>(o_col + 32u * c, o0);
+    tmem_st<16>(o_col + 32u * c + 16u, o1);
+  }
+  tmem_wait_st();
+  return true;
+}
+
 template <bool DUALK, int LAYOUT>
 __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, int warp, int lane,
                           const WaitCtl wc) {
@@ -671,104 +797,138 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
   const uint32_t lanes = (uint32_t)(32 * w) << 16;
   const uint32_t ts = tmem + lanes + kColS + 128u * t, to = tmem + lanes + kColO + 128u * t;
   const float qs = p.qscale;
-  int sc = 0, oc[2] = {0, 0}, base = 0;
+  uint32_t sp = 0;           // phases of s_full, bit b
+  uint32_t of = 0;           // phases of o_full, bit i
+  int od[2] = {0, 0}, base = 0;  // products of each half so far; ring loads before the item
   for (int it = 0;; ++it) {
-    if (!warp_wait(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc, lane)) return;
+    if (!warp_poll(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc)) return;
     const Item x = sm.item[it & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.it_empty[it & 1]);
     if (x.kb1 < 0) return;
-    const int n = x.kb1 - x.kb0, mine = DUALK ? (n - t + 1) / 2 : n;
+    const int n = x.kb1 - x.kb0, mine = halves_of<DUALK>(n, x.halves, t);
     const int first_tok = x.tok0 + (DUALK ? 0 : t * (kRows >> p.g_log2));
     const int tok = first_tok + (r >> p.g_log2);
     const bool idle = first_tok + ((w * 32) >> p.g_log2) >= x.T;  // no row of this warp is one of the sequence
     float m = -INFINITY, l = 0.f;
-    for (int jj = 0; jj < mine; ++jj) {
-      const int j = DUALK ? 2 * jj + t : jj, k0 = (x.kb0 + j) * kBN;
-      const bool masked = block_masked(p, x, k0);
-      if (masked) {
-        const int vi = base + (DUALK ? min(n, j + 2) + j : 2 * j + 1);  // the load that brought V
-        if (!warp_wait(&sm.kv_full[vi % ST], (uint32_t)((vi / ST) & 1), wc, lane)) return;
-        if (clean_v(sm.kv[vi % ST], r, &sm.poison[it & 1], it + 1))
+    // The softmax of step g.  Steps with masked places come last and have code of
+    // their own: one loop for both took 1.25 times as long, masked or not.
+    auto step = [&](auto is_masked, int g) -> bool {
+      constexpr bool MASKED = decltype(is_masked)::value;
+      const int b = g % kNB, j = DUALK ? 2 * (g / kNB) + t : g / kNB, k0 = (x.kb0 + j) * kBN + b * kHN;
+      if constexpr (MASKED) {
+        const int i = base + v_load<DUALK>(n, j);
+        if (!warp_poll(&sm.kv_full[i % ST], (uint32_t)((i / ST) & 1), wc)) return false;
+        if (clean_v(sm.kv[i % ST] + b * (kHN * 128), r, &sm.poison[it & 1], it + 1))
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      if (!warp_wait(&sm.s_full[t], (uint32_t)(sc & 1), wc, lane)) return;
-      ++sc;
+      if (!warp_poll(&sm.s_full[t][b], (sp >> b) & 1u, wc)) return false;
+      sp ^= 1u << b;
       tc_fence_after();
       if (!idle) {
-        float s[128];
+        const uint32_t tsb = ts + 64u * b;
+        f32x2 s[kHN / 2];
         {
-          uint32_t u[4][32];
+          uint32_t u[kHN / 32][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_nowait<32>(ts + 32u * c, u[c]);
+          for (int c = 0; c < kHN / 32; ++c) tmem_ld_nowait<32>(tsb + 32u * c, u[c]);
           tmem_wait_ld();
+          if constexpr (MASKED) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(u[c >> 5][c & 31]);
-        }
-        if (masked) {
+            for (int c = 0; c < kHN / 32; ++c) {
+              const uint32_t bits = sees(p, x, tok, k0 + 32 * c);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t bits = sees(p, x, tok, k0 + 32 * c);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((bits >> e) & 1u)) s[32 * c + e] = -INFINITY;
+              for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) u[c][e] = 0xff800000u;  // -inf
+            }
           }
+#pragma unroll
+          for (int c = 0; c < kHN / 2; ++c)
+            s[c] = pair(__uint_as_float(u[c >> 4][2 * c & 31]), __uint_as_float(u[c >> 4][(2 * c + 1) & 31]));
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        float2 mx[4] = {both(s[0]), both(s[1]), both(s[2]), both(s[3])};
 #pragma unroll
-        for (int c = 4; c < 128; c += 4)
+        for (int c = 4; c < kHN / 2 - 4; c += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[c + e]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = both(s[c + e]), z = both(s[c + 4 + e]);
+            mx[e].x = max3_nan(mx[e].x, y.x, z.x);
+            mx[e].y = max3_nan(mx[e].y, y.y, z.y);
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = both(s[kHN / 2 - 4 + e]);
+          mx[e].x = max_nan(mx[e].x, y.x);
+          mx[e].y = max_nan(mx[e].y, y.y);
+        }
+        const float top = max3_nan(max3_nan(mx[0].x, mx[0].y, mx[1].x), max3_nan(mx[1].y, mx[2].x, mx[2].y),
+                                   max_nan(mx[3].x, mx[3].y)) * qs;
         const bool up = top > m + kSlack;
         if (__any_sync(kFull, up)) {
           const float mn = up ? top : m;
           const float a = up ? ex2(m - mn) : 1.f;
           m = mn;
           l *= a;
-          if (jj > 0) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld_nowait<32>(to + 32u * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              uint32_t h0[16], h1[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                h0[e] = o[e];
-                h1[e] = o[16 + e];
-              }
-              tmem_st<16>(to + 32u * c, h0);
-              tmem_st<16>(to + 32u * c + 16u, h1);
-            }
-          }
+          if (g > 0 && !rescale(to, a, &sm.o_done[t], (uint32_t)((od[t] + g - 1) & 1), wc)) return false;
         }
+        // a NaN or +inf logit makes the row NaN, whichever way its exponential is taken
+        if (!(top < INFINITY)) l = NAN;
         const float mu = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const f32x2 mu2 = pair(mu, mu), qs2 = pair(qs, qs);
+        // of every 8 pairs of weights, the first `fma` go to the FMA pipe
+        auto weights = [&](int fma) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pw[16];
+          for (int c = 0; c < kHN / 32; ++c) {
+            uint32_t pw[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float &x0 = s[32 * c + e], &x1 = s[32 * c + e + 1];
-            fma2(x0, x1, qs, mu);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-            sum[e & 2] += x0;
-            sum[(e & 2) + 1] += x1;
-            pw[e / 2] = pack_bf16(x0, x1);
+            for (int e = 0; e < 16; ++e) {
+              f32x2 &v = s[16 * c + e];
+              v = fma2(v, qs2, mu2);
+              if (e % 8 < fma) {
+                v = exp2_fma(v);
+              } else {
+                const float2 y = both(v);
+                v = pair(ex2(y.x), ex2(y.y));
+              }
+              const float2 y = both(v);
+              pw[e] = pack_bf16(y.x, y.y);
+            }
+            tmem_st<16>(tsb + 16u * c, pw);
           }
-          tmem_st<16>(ts + 16u * c, pw);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        };
+        weights(MASKED ? 0 : kFmaOf8);  // masked logits need exact zeros
         tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
+        // the sum is not on the way to the next product
+        f32x2 sum[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < kHN / 2; c += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], s[c + e]);
+        const float2 all = both(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l += all.x + all.y;
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[t]);
+      return true;
+    };
+    int clear = 0;  // steps without masked places
+    {
+      const int keys = p.mask != nullptr ? x.ctx : x.ctx + x.tok0 + 1;  // seen by every row
+      const int whole = keys / kHN - x.kb0 * kNB;                         // steps of the item below them
+      const int blocks = whole > 0 ? whole / kNB : 0, rest = whole > 0 ? whole % kNB : 0;
+      clear = DUALK ? kNB * (max(0, blocks - t + 1) / 2) + ((blocks & 1) == t ? rest : 0) : whole;
+      clear = max(0, min(mine, clear));
     }
+    int g = 0;
+    for (; g < clear; ++g)
+      if (!step(std::false_type{}, g)) return;
+    for (; g < mine; ++g)
+      if (!step(std::true_type{}, g)) return;
     base += 2 * n;
 
     // output: O / l, or O, m and l as a partial
@@ -778,17 +938,21 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
       sm.ml[t][1][r] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ml_full);
-      if (!warp_wait(&sm.ml_full, (uint32_t)(it & 1), wc, lane)) return;
+      if (!warp_poll(&sm.ml_full, (uint32_t)(it & 1), wc)) return;
       const float m0 = sm.ml[0][0][r], m1 = sm.ml[1][0][r];
       m = fmaxf(m0, m1);
       f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
       f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
       l = sm.ml[0][1][r] * f0 + sm.ml[1][1][r] * f1;
-      for (int i = 0; i < 2 && i < n; ++i, ++oc[i - 1])
-        if (!warp_wait(&sm.o_full[i], (uint32_t)(oc[i] & 1), wc, lane)) return;
-    } else {
-      if (!warp_wait(&sm.o_full[t], (uint32_t)(oc[t] & 1), wc, lane)) return;
-      ++oc[t];
+    }
+    // the last product of this half (DUALK: of both) must have been added to O
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int hi = halves_of<DUALK>(n, x.halves, i);
+      od[i] += hi;
+      if (hi == 0) continue;
+      if ((DUALK || i == t) && !warp_poll(&sm.o_full[i], (of >> i) & 1u, wc)) return;
+      of ^= 1u << i;
     }
     tc_fence_after();
     if (!idle) {
@@ -822,7 +986,8 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
           float y[32];  // a copy, so that o itself stays in registers
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = o[e];
-          add_not_finite<LAYOUT>(p, x, tok, d0, y);
+          const Item z = x;
+          add_not_finite<LAYOUT>(p, z, tok, d0, y);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = y[e];
         }
@@ -852,7 +1017,7 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
       // the next item's products may overwrite O once both groups have read it
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_read);
-      if (!warp_wait(&sm.o_read, (uint32_t)(it & 1), wc, lane)) return;
+      if (!warp_poll(&sm.o_read, (uint32_t)(it & 1), wc)) return;
     }
   }
 }
@@ -867,21 +1032,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < Cfg::ST; ++i) {
       mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_empty[i], 1);
+      mbar_init(&sm.kv_empty[i], DUALK ? 1 : 2);
     }
     mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sm.s_full[i][b], 1);
+        mbar_init(&sm.p_full[i][b], 4);
+      }
+      mbar_init(&sm.o_done[i], 1);
       mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.drain[i], 1);
       mbar_init(&sm.it_full[i], 1);
-      mbar_init(&sm.it_empty[i], kSoftWarps + 1);
+      mbar_init(&sm.it_empty[i], kSoftWarps + 2);
       sm.poison[i] = 0;
     }
     mbar_init(&sm.ml_full, kSoftWarps);
     mbar_init(&sm.o_read, kSoftWarps);
-    mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -892,15 +1060,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   const uint32_t tmem = sm.tmem_base;
   const WaitCtl wc = wait_ctl(&sm.abort_flag, p.status, 0);
   if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     soft_role<DUALK, LAYOUT>(p, sm, tmem, warp, lane, wc);
-  } else if (warp == kLoadWarp) {
-    if constexpr (LAYOUT == kPacked)
-      load_role<DUALK, LAYOUT, PromptCursor<DUALK>>(p, sm, lane, wc);
-    else
-      load_role<DUALK, LAYOUT, TreeCursor<DUALK, LAYOUT>>(p, sm, lane, wc);
   } else {
-    if (lane == 0) mma_role<DUALK>(p, sm, tmem, wc);
-    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+    if (warp == kLoadWarp) {
+      if constexpr (LAYOUT == kPacked)
+        load_role<DUALK, LAYOUT, PromptCursor<DUALK>>(p, sm, lane, wc);
+      else
+        load_role<DUALK, LAYOUT, TreeCursor<DUALK, LAYOUT>>(p, sm, lane, wc);
+    } else if (warp == kIssueWarp || warp == kIssueWarp + 2) {
+      mma_role<DUALK>(p, sm, tmem, (warp - kIssueWarp) >> 1, lane, wc);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1060,6 +1231,10 @@ cudaError_t launch_attend(const AttendParams &p, int grid, cudaStream_t st) {
   if (attr_dev != dev) {
     e = cudaFuncSetAttribute(attend_kernel<DUALK, LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // the register split draws on what the block is launched with
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, attend_kernel<DUALK, LAYOUT>)) != cudaSuccess) return e;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
     attr_dev = dev;
   }
   attend_kernel<DUALK, LAYOUT><<<grid, kAtThreads, smem, st>>>(p);
