@@ -602,7 +602,8 @@ tria_status tria_tree_attention(const tria_stats *stats, const tria_cache_view *
  * Workspace: tria_commit_workspace_size bytes (256-byte aligned), all zero
  * before its first use (it holds arrival counts that every call leaves at
  * zero); its first 256 bytes hold the status flags.  Calls that may overlap
- * need separate workspaces.  Errors: INVALID_ARG, WORKSPACE, CUDA.
+ * need separate workspaces.  Errors: INVALID_ARG, UNSUPPORTED (max_accept x KV
+ * heads past 2^31), WORKSPACE, CUDA.
  */
 tria_status tria_commit_workspace_size(const tria_stats *stats, const tria_cache_view *cache,
                                        size_t *bytes);

@@ -418,21 +418,35 @@ def tria_decode_attention(stats, cache, layer, q, scale, out, workspace, lse=Non
                                        _stream(stream)), "tria_decode_attention")
 
 
-def _on_device(where, **tensors):
-    """The serving operators take plain pointers: each tensor must lie on the
-    current device, in the type and layout that the kernels read."""
+def _on_device(where, *tensors):
+    """The serving operators take plain pointers: every (name, tensor or None,
+    types, dimensions, contiguous) must lie on the current device, in the type
+    and layout that the kernels read.  Returns the device's index."""
     import torch
 
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, (t, dtypes, dim, contiguous) in tensors.items():
+    dev = None
+    for name, t, dtypes, dim, contiguous in tensors:
         if t is None:
             continue
-        if t.get_device() != dev or dev < 0:
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        if d < 0 or d != dev:
             raise TriaError(1, f"{where}: {name} must be on the current CUDA device")
         if t.dtype not in dtypes or t.dim() != dim:
             raise TriaError(1, f"{where}: {name} must have {dim} dimensions and type {dtypes[0]}")
         if contiguous and not t.is_contiguous():
             raise TriaError(1, f"{where}: {name} must be contiguous")
+    if dev != torch.cuda.current_device():
+        raise TriaError(1, f"{where}: the tensors must be on the current CUDA device")
+    return dev
+
+
+def _stream_on(stream, dev):
+    """The raw stream to launch on: the device's current one by default."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _row_strides(t):
@@ -461,18 +475,20 @@ def tria_prompt_attention(desc, q, k, v, seq_starts, scale, out, workspace, lse=
     import torch
 
     bf, where = (torch.bfloat16,), "tria_prompt_attention"
-    _on_device(where, q=(q, bf, 3, False), k=(k, bf, 3, False), v=(v, bf, 3, False),
-               seq_starts=(seq_starts, (torch.int32,), 1, True), out=(out, bf, 3, True),
-               lse=(lse, (torch.float32,), 2, True), workspace=(workspace, (torch.uint8,), 1, True))
+    dev = _on_device(where, ("q", q, bf, 3, False), ("k", k, bf, 3, False), ("v", v, bf, 3, False),
+                     ("seq_starts", seq_starts, (torch.int32,), 1, True), ("out", out, bf, 3, True),
+                     ("lse", lse, (torch.float32,), 2, True),
+                     ("workspace", workspace, (torch.uint8,), 1, True))
     n, hq, hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
-    if (q.shape != (n, hq, 128) or k.shape != (n, hkv, 128) or v.shape != k.shape or out.shape != q.shape
+    kv = (n, hkv, 128)
+    if (q.shape != (n, hq, 128) or k.shape != kv or v.shape != kv or out.shape != q.shape
             or seq_starts.shape[0] < 2 or (lse is not None and lse.shape != (n, hq))):
         raise TriaError(1, f"{where}: shapes")
     _check(lib().tria_prompt_attention(
         ctypes.byref(desc), q.data_ptr(), *_row_strides(q), k.data_ptr(), *_row_strides(k),
         v.data_ptr(), *_row_strides(v), n, seq_starts.data_ptr(), seq_starts.shape[0] - 1,
-        scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)),
-        where)
+        scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
+        _stream_on(stream, dev)), where)
 
 
 def tria_tree_workspace_size(stats, cache, max_draft) -> int:
@@ -493,9 +509,10 @@ def tria_tree_attention(stats, cache, layer, q, draft_starts, max_draft, scale, 
 
     bf, where = (torch.bfloat16,), "tria_tree_attention"
     words = (torch.int32, torch.uint32)
-    _on_device(where, q=(q, bf, 3, False), draft_starts=(draft_starts, (torch.int32,), 1, True),
-               out=(out, bf, 3, True), mask=(mask, words, 2, True),
-               lse=(lse, (torch.float32,), 2, True), workspace=(workspace, (torch.uint8,), 1, True))
+    dev = _on_device(where, ("q", q, bf, 3, False),
+                     ("draft_starts", draft_starts, (torch.int32,), 1, True), ("out", out, bf, 3, True),
+                     ("mask", mask, words, 2, True), ("lse", lse, (torch.float32,), 2, True),
+                     ("workspace", workspace, (torch.uint8,), 1, True))
     n, hq = q.shape[0], stats.desc.n_q_heads
     if (q.shape != (n, hq, 128) or out.shape != q.shape or draft_starts.shape[0] != cache.view.n_seq + 1
             or (mask is not None and mask.shape[0] != n) or (lse is not None and lse.shape != (n, hq))):
@@ -503,7 +520,8 @@ def tria_tree_attention(stats, cache, layer, q, draft_starts, max_draft, scale, 
     _check(lib().tria_tree_attention(
         stats.handle, ctypes.byref(cache.view), layer, q.data_ptr(), *_row_strides(q), n,
         draft_starts.data_ptr(), max_draft, _ptr(mask), 0 if mask is None else mask.shape[1], scale,
-        out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+        out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream_on(stream, dev)),
+        where)
 
 
 def tria_commit_workspace_size(stats, cache) -> int:
@@ -520,14 +538,16 @@ def tria_tree_commit(stats, cache, accepted, n_accepted, layer0, layer1, workspa
     import torch
 
     i32, where = (torch.int32,), "tria_tree_commit"
-    _on_device(where, accepted=(accepted, i32, 2, True), n_accepted=(n_accepted, i32, 1, True),
-               workspace=(workspace, (torch.uint8,), 1, True))
+    dev = _on_device(where, ("accepted", accepted, i32, 2, True),
+                     ("n_accepted", n_accepted, i32, 1, True),
+                     ("workspace", workspace, (torch.uint8,), 1, True))
     n = cache.view.n_seq
     if accepted.shape[0] != n or n_accepted.shape[0] != n:
         raise TriaError(1, f"{where}: shapes")
     _check(lib().tria_tree_commit(stats.handle, ctypes.byref(cache.view), accepted.data_ptr(),
                                   n_accepted.data_ptr(), accepted.shape[1], layer0, layer1,
-                                  workspace.data_ptr(), workspace.numel(), _stream(stream)), where)
+                                  workspace.data_ptr(), workspace.numel(), _stream_on(stream, dev)),
+           where)
 
 
 def tria_fork_workspace_size(stats, cache) -> int:
@@ -544,13 +564,13 @@ def tria_fork_sequences(stats, cache, src, dst, layer0, layer1, workspace, strea
     import torch
 
     where = "tria_fork_sequences"
-    _on_device(where, workspace=(workspace, (torch.uint8,), 1, True))
+    dev = _on_device(where, ("workspace", workspace, (torch.uint8,), 1, True))
     if len(src) != len(dst):
         raise TriaError(1, f"{where}: src and dst must have the same length")
     a, b = (np.ascontiguousarray(x, dtype=np.int32) for x in (src, dst))
     _check(lib().tria_fork_sequences(stats.handle, ctypes.byref(cache.view), a.ctypes.data,
                                      b.ctypes.data, len(a), layer0, layer1, workspace.data_ptr(),
-                                     workspace.numel(), _stream(stream)), where)
+                                     workspace.numel(), _stream_on(stream, dev)), where)
 
 
 def tria_read_device_status(workspace, stream=None) -> int:

@@ -80,14 +80,17 @@ struct LayerPtrs {
 
 // ---------------------------------------------------------------------------
 // Accepted path: row N + accepted[j] -> row N + j, j ascending.  One block
-// moves the K or the V rows of one (sequence, layer), all KV heads, in chunks
-// of kMoveU x 256 pieces: a chunk is read into registers, a barrier, written.
+// moves the K and V rows of one (sequence, layer), all KV heads, in chunks of
+// kMoveU x 256 pieces of each: a chunk is read into registers, a barrier, written.
 // In place this is safe: accepted[j] >= j, so a later chunk's sources lie
 // above every destination already written, and within a chunk every read
-// comes before the barrier.
+// comes before the barrier.  The path is checked by the threads while the
+// first chunk's rows are on their way (a source out of range is not read), and
+// one barrier serves both.
 // ---------------------------------------------------------------------------
-constexpr int kMoveU = 8;
-constexpr int kMoveRows = kMoveU * kMoveThreads / kPieces;  // rows of a chunk: 128
+constexpr int kMoveU = 4;
+constexpr int kMoveRows = kMoveU * kMoveThreads / kPieces;  // rows of a chunk: 64
+constexpr int kRowStep = kMoveThreads / kPieces;            // rows of one pass of the block: 16
 
 struct CommitParams {
   RowsView view;
@@ -100,82 +103,97 @@ struct CommitParams {
   int32_t *status;
 };
 
-__global__ void __launch_bounds__(kMoveThreads) commit_kernel(const __grid_constant__ CommitParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) commit_kernel(const __grid_constant__ CommitParams p) {
   const RowsView &v = p.view;
-  const int s = blockIdx.x / (2 * p.nl), l = (blockIdx.x / 2) % p.nl, is_v = blockIdx.x & 1;
-  const int tid = threadIdx.x, layer = p.layer0 + l;
+  const int s = blockIdx.x / p.nl, l = blockIdx.x % p.nl;
+  const int tid = threadIdx.x, layer = p.layer0 + l, hkv = v.hkv;
   const int N = view_len(v, s, layer);
   const int n = p.n_accepted[s];
   const int32_t *acc = p.accepted + (int64_t)s * p.max_accept;
   const bool count_ok = n >= 0 && n <= p.max_accept;
-  bool asc = count_ok;
+  const int room = N >= 0 ? v.max_seq_len - N : 0;  // drafted slots behind the committed rows
+  uint16_t *kp = p.at.k[l] + (tid % kPieces) * 8, *vp = p.at.v[l] + (tid % kPieces) * 8;
+  int32_t *pos = (v.positions == nullptr || tid % kPieces != 0)
+                     ? nullptr
+                     : v.positions + ((int64_t)s * v.n_layers + layer) * hkv * v.max_seq_len + max(N, 0);
+  const int rows = count_ok && N >= 0 ? n * hkv : 0;  // at most INT32_MAX - kMoveRows (host)
+  const int step_j = kRowStep / hkv, step_h = kRowStep % hkv;
+  bool path_ok = count_ok, ok = count_ok && N >= 0, bad = false;
   int last = -1;
-  if (count_ok) {
-    for (int j = tid; j < n; j += kMoveThreads) asc = asc && acc[j] > (j > 0 ? acc[j - 1] : -1);
-    if (n > 0) last = acc[n - 1];
-  }
-  const bool path_ok = __syncthreads_and(asc) != 0;
-  const bool ok = path_ok && N >= 0 && last < v.max_seq_len - N;
-  if (!ok) {
-    if (tid == 0) atomicOr(p.status, 1);
-  } else {
-    uint16_t *base = is_v ? p.at.v[l] : p.at.k[l];
-    int32_t *pos = (is_v || v.positions == nullptr)
-                       ? nullptr
-                       : v.positions + ((int64_t)s * v.n_layers + layer) * v.hkv * v.max_seq_len;
-    const int64_t rows = (int64_t)n * v.hkv;
-    for (int64_t r0 = 0; r0 < rows; r0 += kMoveRows) {
-      uint4 x[kMoveU];
-      int32_t xp[kMoveU];
-      uint32_t moves = 0;
-      bool bad = false;
+  for (int r0 = 0; r0 == 0 || (ok && r0 < rows); r0 += kMoveRows) {
+    uint4 xk[kMoveU], xv[kMoveU];
+    int64_t to[kMoveU];
+    int32_t xp[kMoveU];
+    uint32_t moves = 0;
+    const int first = r0 + tid / kPieces;
+    int j = first / hkv, h = first % hkv;
 #pragma unroll
-      for (int u = 0; u < kMoveU; ++u) {
-        const int64_t r = r0 + (u * kMoveThreads + tid) / kPieces;
-        if (r < rows) {
-          const int j = (int)(r / v.hkv), h = (int)(r % v.hkv), a = acc[j];
-          int64_t from, to;
-          if (a != j) {
-            const bool there = view_row(v, s, h, N + a, &from) && view_row(v, s, h, N + j, &to);
-            if (there) {
-              x[u] = *reinterpret_cast<const uint4 *>(base + from + (tid % kPieces) * 8);
-              moves |= 1u << u;
-            } else {
-              bad = true;
-            }
-            if (pos != nullptr && tid % kPieces == 0) xp[u] = pos[(int64_t)h * v.max_seq_len + N + a];
+    for (int u = 0; u < kMoveU; ++u) {
+      if (first + u * kRowStep < rows) {
+        const int a = acc[j];
+        if (a > j && a < room) {  // a = j stays; anything else is no path
+          int64_t from;
+          if (view_row(v, s, h, N + a, &from) && view_row(v, s, h, N + j, &to[u])) {
+            xk[u] = *reinterpret_cast<const uint4 *>(kp + from);
+            xv[u] = *reinterpret_cast<const uint4 *>(vp + from);
+            moves |= 1u << u;
+          } else {
+            bad = true;
           }
+          if (pos != nullptr) xp[u] = pos[(int64_t)h * v.max_seq_len + a];
         }
       }
-      if (bad) atomicOr(p.status, 1);
+      j += step_j;
+      h += step_h;
+      if (h >= hkv) {
+        h -= hkv;
+        ++j;
+      }
+    }
+    if (r0 == 0) {
+      bool asc = count_ok;
+      if (count_ok) {
+        for (int i = tid; i < n; i += kMoveThreads) asc = asc && acc[i] > (i > 0 ? acc[i - 1] : -1);
+        if (n > 0) last = acc[n - 1];
+      }
+      path_ok = __syncthreads_and(asc) != 0;
+      ok = path_ok && N >= 0 && last < room;
+    } else {
       __syncthreads();
+    }
+    if (ok) {
+      j = first / hkv;
+      h = first % hkv;
 #pragma unroll
       for (int u = 0; u < kMoveU; ++u) {
-        if (!((moves >> u) & 1u)) continue;
-        const int64_t r = r0 + (u * kMoveThreads + tid) / kPieces;
-        const int j = (int)(r / v.hkv), h = (int)(r % v.hkv);
-        int64_t to;
-        view_row(v, s, h, N + j, &to);
-        *reinterpret_cast<uint4 *>(base + to + (tid % kPieces) * 8) = x[u];
-        if (pos != nullptr && tid % kPieces == 0) pos[(int64_t)h * v.max_seq_len + N + j] = xp[u];
+        if ((moves >> u) & 1u) {
+          *reinterpret_cast<uint4 *>(kp + to[u]) = xk[u];
+          *reinterpret_cast<uint4 *>(vp + to[u]) = xv[u];
+        }
+        if (pos != nullptr && first + u * kRowStep < rows && acc[j] > j) pos[(int64_t)h * v.max_seq_len + j] = xp[u];
+        j += step_j;
+        h += step_h;
+        if (h >= hkv) {
+          h -= hkv;
+          ++j;
+        }
       }
     }
   }
-  if (!p.grow) return;
-  // every block of the sequence has read its length before it arrives here
-  __shared__ int s_last;
-  __syncthreads();
-  if (tid == 0) s_last = atom_add_acq_rel(p.arrived + s, 1u) == (uint32_t)(2 * p.nl - 1) ? 1 : 0;
-  __syncthreads();
-  if (!s_last) return;
+  if (ok ? bad : tid == 0) atomicOr(p.status, 1);
+  if (!p.grow || tid >= 32) return;
+  // every thread has read the length before the barrier, so this block may arrive
+  int is_last = 0;
+  if (tid == 0) is_last = atom_add_acq_rel(p.arrived + s, 1u) == (uint32_t)(p.nl - 1) ? 1 : 0;
+  if (!__shfl_sync(kFull, is_last, 0)) return;
   if (tid == 0) p.arrived[s] = 0u;
   if (!path_ok) return;
   if (v.lens_l == 0) {
     if (tid == 0 && ok) v.lens[s] = N + n;
   } else {
-    for (int i = tid; i < p.nl; i += kMoveThreads) {
-      const int nl = view_len(v, s, p.layer0 + i);
-      if (nl >= 0 && last < v.max_seq_len - nl) v.lens[(int64_t)s * v.lens_s + p.layer0 + i] = nl + n;
+    for (int i = tid; i < p.nl; i += 32) {
+      const int len = view_len(v, s, p.layer0 + i);
+      if (len >= 0 && last < v.max_seq_len - len) v.lens[(int64_t)s * v.lens_s + p.layer0 + i] = len + n;
     }
   }
 }
@@ -220,7 +238,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
   const int nt = min(kForkRows, N - t0);
   uint16_t *base = is_v ? p.at.v[l] : p.at.k[l];
   const bool paged = v.layout == TRIA_LAYOUT_PAGED;
-  const int bs = v.block_size;
+  const int bs = v.block_size, bs_log2 = __ffs(bs) - 1;  // a power of two
   const int b0 = paged ? t0 / bs : 0, nb = paged ? (t0 + nt - 1) / bs - b0 + 1 : 1;
   __shared__ int64_t s_from[kForkBlocks], s_to[kForkDst][kForkBlocks];
   __shared__ uint32_t s_need[kForkBlocks];
@@ -251,7 +269,8 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
       }
       s_need[tid] = need;
     }
-    __syncthreads();
+    // nothing to copy where every destination shares the chunk's blocks
+    if (!__syncthreads_or(tid < nb && s_need[tid] != 0)) continue;
     const int pieces = nt * v.hkv * kPieces;  // at most 64 x hkv x 16; hkv <= INT32_MAX / 1024 (host)
     for (int i0 = tid; i0 < pieces; i0 += kForkU * kMoveThreads) {
       uint4 x[kForkU];
@@ -263,8 +282,8 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
         meta[u] = 0;
         if (i < pieces) {
           const int row = i / kPieces, t = row / v.hkv, h = row - t * v.hkv;
-          const int b = paged ? (t0 + t) / bs - b0 : 0;
-          const int in = paged ? (t0 + t) % bs : t0 + t;
+          const int b = paged ? ((t0 + t) >> bs_log2) - b0 : 0;
+          const int in = paged ? (t0 + t) & (bs - 1) : t0 + t;
           const uint32_t need = s_need[b];
           off[u] = (int64_t)h * v.s_head + (int64_t)in * v.s_tok + (i % kPieces) * 8;
           meta[u] = need | ((uint32_t)b << 8);
@@ -282,8 +301,10 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
   if (is_v || v.positions == nullptr) return;
   const int64_t unit = (int64_t)v.hkv * v.max_seq_len;
   const int32_t *from = v.positions + ((int64_t)s * v.n_layers + layer) * unit;
-  for (int i = tid; i < nt * v.hkv; i += kMoveThreads) {
-    const int64_t o = (int64_t)(i / nt) * v.max_seq_len + t0 + i % nt;
+  const int t = tid % kForkRows;
+  if (t >= nt) return;
+  for (int h = tid / kForkRows; h < v.hkv; h += kMoveThreads / kForkRows) {
+    const int64_t o = (int64_t)h * v.max_seq_len + t0 + t;
     const int32_t x = from[o];
     for (int d = d0; d < d1; ++d)
       v.positions[((int64_t)p.dst[d] * v.n_layers + layer) * unit + o] = x;
@@ -330,6 +351,8 @@ tria_status tria_tree_commit(const tria_stats *stats, const tria_cache_view *cac
   if (accepted == nullptr || n_accepted == nullptr || max_accept < 1 ||
       (reinterpret_cast<uintptr_t>(accepted) & 3u) || (reinterpret_cast<uintptr_t>(n_accepted) & 3u))
     return TRIA_ERR_INVALID_ARG;
+  // the kernel counts rows of 32 bits
+  if ((int64_t)max_accept * d.n_kv_heads > INT32_MAX - kMoveRows) return TRIA_ERR_UNSUPPORTED;
   const tria_status sw = check_header_workspace(ws, ws_bytes, commit_ws_bytes(cache));
   if (sw != TRIA_OK) return sw;
   layer_ptrs(cache, layer0, layer1, &p.at);
@@ -341,7 +364,7 @@ tria_status tria_tree_commit(const tria_stats *stats, const tria_cache_view *cac
   p.grow = moves_lens(p.view, layer1) ? 1 : 0;
   p.arrived = reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
   p.status = status_of(ws);
-  const unsigned blocks = (unsigned)cache->n_seq * (unsigned)p.nl * 2u;
+  const unsigned blocks = (unsigned)cache->n_seq * (unsigned)p.nl;
   commit_kernel<<<blocks, kMoveThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
 }
