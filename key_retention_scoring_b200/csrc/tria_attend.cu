@@ -50,15 +50,17 @@ namespace {
 using namespace dev;
 using namespace tc;
 
-// Waits of the pipeline: the threads sleep in the barrier unit, at most hint_ns
-// at a time; the timer and the abort flag are looked at after a sleep that ran
-// out.
+// Waits of the pipeline: the threads sleep in the barrier unit (polling took
+// shared-memory cycles from the products: 1.25 times the time); the clock and
+// the abort flag are looked at after a sleep that ran out.  The limit counts
+// SM cycles at 2 GHz, which is never short: the clock goes one way, while a
+// reading of the global timer was once seen to step back.
 __device__ __forceinline__ bool poll_on(uint32_t bar, uint32_t parity, const WaitCtl &w) {
-  const uint64_t t0 = global_timer();
+  const long long t0 = clock64();
   for (;;) {
     if (mbar_try_sleep(bar, parity, w.hint_ns)) return true;
     if (*w.abort_flag) return false;
-    if (global_timer() - t0 > w.limit_ns) {
+    if (clock64() - t0 > (long long)(2 * w.limit_ns)) {
       flag_expiry(w);
       return false;
     }
@@ -121,22 +123,29 @@ struct AttendParams {
 // One piece of work: rows of tokens [tok0, ..) of (s, h) against key blocks [kb0, kb1).
 struct Item {
   int s, h, tok0, T, ctx, kb0, kb1, slot;      // slot: -1 writes the output, else a partial
-  int halves;                                  // half blocks with keys that some row sees
+  int steps;                                   // steps with keys that some row sees
   int64_t row0;                                // first row of the sequence in q and out
 };
 
+// The ring of K and V tiles.  DUALQ: both halves of the CTA use every tile.
+// DUALK: each half has a ring of its own for its key blocks, so that it waits
+// for loads in the order in which it used the stages before (the phase of a
+// stage that the other half still waits for could not be told apart).
 template <bool DUALK>
 struct AtCfg {
   static constexpr int QT = DUALK ? 1 : 2;           // tiles of rows
   static constexpr int ROWS = 128 * QT;
-  static constexpr int ST = 5;                       // ring stages (K or V tiles)
+  static constexpr int ST = DUALK ? 3 : 5;           // stages of a ring
+  static constexpr int RINGS = DUALK ? 2 : 1;
+  static __device__ __forceinline__ int stage(int t, int i) { return (DUALK ? ST * t : 0) + i % ST; }
+  static __device__ __forceinline__ uint32_t phase(int i) { return (uint32_t)((i / ST) & 1); }
 };
 
 template <bool DUALK>
 struct AtSmem {
   alignas(1024) uint8_t q[AtCfg<DUALK>::QT][kTile];
-  alignas(1024) uint8_t kv[AtCfg<DUALK>::ST][kTile];
-  alignas(8) uint64_t kv_full[AtCfg<DUALK>::ST], kv_empty[AtCfg<DUALK>::ST];
+  alignas(1024) uint8_t kv[AtCfg<DUALK>::RINGS * AtCfg<DUALK>::ST][kTile];
+  alignas(8) uint64_t kv_full[AtCfg<DUALK>::RINGS * AtCfg<DUALK>::ST], kv_empty[AtCfg<DUALK>::RINGS * AtCfg<DUALK>::ST];
   uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_done[2], o_full[2], it_full[2], it_empty[2], ml_full, o_read, drain[2];
   Item item[2];
   float ml[DUALK ? 2 : 1][2][DUALK ? 128 : 1];
@@ -171,27 +180,23 @@ __device__ __forceinline__ int key_blocks(const AttendParams &p, int ctx, int T,
   return (n + kBN - 1) / kBN;
 }
 
-// half blocks of a piece [kb0, kb1) that hold a key some row sees
-__device__ __forceinline__ int half_blocks(const AttendParams &p, const Item &x, int tok_end) {
+// steps of a piece [kb0, kb1) that hold a key some row sees
+__device__ __forceinline__ int item_steps(const AttendParams &p, const Item &x, int tok_end) {
   const int keys = x.ctx + (p.mask != nullptr ? x.T : min(x.T, tok_end));
   return min(kNB * (x.kb1 - x.kb0), (keys - x.kb0 * kBN + kHN - 1) / kHN);
 }
 
-// Halves of a piece that half t of the CTA works on, and where the ring's loads
-// hold K and V of block j (the order in which mma_role uses them).
+// Steps of a piece of n blocks that half t of the CTA works on, and its blocks.
+// Its ring holds K of its block b in load 2 b and V in load 2 b + 1, counted
+// from the item's first load.
 template <bool DUALK>
-__device__ __forceinline__ int halves_of(int n, int halves, int t) {
-  if (!DUALK) return halves;
-  const int blocks = (n - t + 1) / 2;
-  return kNB * blocks - (((n - 1) & 1) == t ? kNB * n - halves : 0);
+__device__ __forceinline__ int blocks_of(int n, int t) {
+  return DUALK ? (n - t + 1) / 2 : n;
 }
 template <bool DUALK>
-__device__ __forceinline__ int k_load(int n, int j) {
-  return DUALK ? (j < 2 ? j : 2 * j - 1) : 2 * j;
-}
-template <bool DUALK>
-__device__ __forceinline__ int v_load(int n, int j) {
-  return DUALK ? min(n, j + 2) + j : 2 * j + 1;
+__device__ __forceinline__ int steps_of(int n, int steps, int t) {
+  if (!DUALK) return steps;
+  return kNB * blocks_of<DUALK>(n, t) - (((n - 1) & 1) == t ? kNB * n - steps : 0);
 }
 
 // key blocks of all (KV head, tile of ROWS rows) units of a sequence
@@ -288,7 +293,7 @@ struct PromptCursor {
     x.tok0 = lo * tpi(p);
     x.kb0 = 0;
     x.kb1 = key_blocks(p, 0, x.T, x.tok0 + tpi(p));
-    x.halves = half_blocks(p, x, x.tok0 + tpi(p));
+    x.steps = item_steps(p, x, x.tok0 + tpi(p));
     x.slot = -1;
     return true;
   }
@@ -386,7 +391,7 @@ struct TreeCursor {
     x.row0 = row0;
     x.kb0 = (int)(pos - ub);
     x.kb1 = (int)(min(end, ub + nb) - ub);
-    x.halves = half_blocks(p, x, tok0 + tpi(p));
+    x.steps = item_steps(p, x, tok0 + tpi(p));
     x.slot = x.kb1 - x.kb0 == nb ? -1 : 2 * (int)blockIdx.x + (pieces > 0 ? 1 : 0);
     pos = ub + x.kb1;
     ++pieces;
@@ -413,7 +418,7 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
   const uint64_t qpol = normal_policy();
   Cursor cur;
   cur.init(p, lane);
-  int it = 0, li = 0;
+  int it = 0;
   bool ok = true;
   Item x{};
   auto wait = [&](uint64_t *bar, int phase) {
@@ -428,9 +433,11 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
                ? __ldg(p.view.block_table + (int64_t)x.s * p.view.max_blocks + t / bs)
                : 0;
   };
+  int li[Cfg::RINGS] = {};  // loads of each ring so far
+  // K or V of key block j of the item
   auto load = [&](bool is_v, int j, int n) -> bool {
-    const int stage = li % ST;
-    if (li >= ST && !wait(&sm.kv_empty[stage], li / ST - 1)) return false;
+    const int t = DUALK ? j & 1 : 0, i = li[DUALK ? t : 0], stage = Cfg::stage(t, i);
+    if (i >= ST && !wait(&sm.kv_empty[stage], i / ST - 1)) return false;
     const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
     const uint32_t dst = smem_u32(&sm.kv[stage][0]);
     const int slot0 = (x.kb0 + j) * kBN;
@@ -459,7 +466,7 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
         if (next_j >= 0) next_blk = table(next_j);
       }
     }
-    ++li;
+    ++li[DUALK ? t : 0];
     return true;
   };
   for (;;) {
@@ -485,8 +492,9 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
     const int n = x.kb1 - x.kb0;
     // in the order in which mma_role uses them
     if (DUALK) {
-      ok = load(false, 0, n) && (n < 2 || load(false, 1, n));
-      for (int j = 0; ok && j < n; ++j) ok = load(true, j, n) && (j + 2 >= n || load(false, j + 2, n));
+      for (int j = 0; ok && j < n; j += 2)
+        ok = load(false, j, n) && (j + 1 == n || load(false, j + 1, n)) && load(true, j, n) &&
+             (j + 1 == n || load(true, j + 1, n));
     } else {
       for (int j = 0; ok && j < n; ++j) ok = load(false, j, n) && load(true, j, n);
     }
@@ -494,7 +502,9 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
   }
   if (!ok && lane == 0) {
     // aborted: loads still in flight must land before the block exits
-    for (int j = li > ST ? li - ST : 0; j < li; ++j) mbar_drain(&sm.kv_full[j % ST], (j / ST) & 1, wc.status);
+    for (int t = 0; t < Cfg::RINGS; ++t)
+      for (int i = li[t] > ST ? li[t] - ST : 0; i < li[t]; ++i)
+        mbar_drain(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc.status);
     if (it > 0) mbar_drain(&sm.q_full, (it - 1) & 1, wc.status);
   }
 }
@@ -564,7 +574,6 @@ __device__ __forceinline__ void elect_commit(uint64_t *bar) {
 template <bool DUALK>
 __device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, int t, int lane, const WaitCtl wc) {
   using Cfg = AtCfg<DUALK>;
-  constexpr int ST = Cfg::ST;
   constexpr uint32_t kHalfRows = (kHN * 128) >> 4;  // 64 rows on in a tile, as a descriptor offset
   const uint32_t s_col = tmem + kColS + 128u * t, o_col = tmem + kColO + 128u * t;
   const uint64_t q_at = sw128_desc(smem_u32(&sm.q[DUALK ? 0 : t][0]));
@@ -574,40 +583,40 @@ __device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem
   bool ok = true, issued = false;
   for (int it = 0; ok; ++it) {
     if (!(ok = warp_poll(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc))) break;
-    const int n = sm.item[it & 1].kb1 - sm.item[it & 1].kb0, halves = sm.item[it & 1].halves;
+    const int n = sm.item[it & 1].kb1 - sm.item[it & 1].kb0, steps = sm.item[it & 1].steps;
     const bool end = sm.item[it & 1].kb1 < 0;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.it_empty[it & 1]);
     if (end) break;
     if (!(ok = warp_poll(&sm.q_full, (uint32_t)(it & 1), wc))) break;
-    const int mine = halves_of<DUALK>(n, halves, t);
+    const int mine = steps_of<DUALK>(n, steps, t);
     if (mine == 0 && lane == 0) mbar_arrive(&sm.q_empty);
-    auto kv_wait = [&](int i) { return warp_poll(&sm.kv_full[i % ST], (uint32_t)((i / ST) & 1), wc); };
+    auto kv_wait = [&](int i) { return warp_poll(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc); };
     // S of half block g into buffer g & 1; its last half releases K
     auto qk = [&](int g) {
-      const int i = base + k_load<DUALK>(n, DUALK ? 2 * (g / kNB) + t : g / kNB), b = g % kNB;
+      const int i = base + 2 * (g / kNB), b = g % kNB;
       if (b == 0 && !kv_wait(i)) return false;
-      mma_qk(s_col + 64u * b, q_at, k_at + (uint32_t)((i % ST) * (kTile >> 4)) + b * kHalfRows, kIdescS);
+      mma_qk(s_col + 64u * b, q_at, k_at + (uint32_t)(Cfg::stage(t, i) * (kTile >> 4)) + b * kHalfRows, kIdescS);
       elect_commit(&sm.s_full[t][b]);
-      if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[i % ST]);
+      if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[Cfg::stage(t, i)]);
       if (g + 1 == mine) elect_commit(&sm.q_empty);
       issued = true;
       return true;
     };
     for (int g = 0; ok && g < kNB && g < mine; ++g) ok = qk(g);
     for (int g = 0; ok && g < mine; ++g) {
-      const int b = g % kNB, i = base + v_load<DUALK>(n, DUALK ? 2 * (g / kNB) + t : g / kNB);
+      const int b = g % kNB, i = base + 2 * (g / kNB) + 1;
       if (b == 0 && !(ok = kv_wait(i))) break;
       if (!(ok = warp_poll(&sm.p_full[t][b], (pp >> b) & 1u, wc))) break;
       pp ^= 1u << b;
       tc_fence_after();
-      mma_pv(o_col, s_col + 64u * b, v_at + (uint32_t)((i % ST) * (kTile >> 4)) + b * kHalfRows, kIdescO, g > 0 ? 1u : 0u);
+      mma_pv(o_col, s_col + 64u * b, v_at + (uint32_t)(Cfg::stage(t, i) * (kTile >> 4)) + b * kHalfRows, kIdescO, g > 0 ? 1u : 0u);
       if (kNB > 1) elect_commit(&sm.o_done[t]);
-      if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[i % ST]);
+      if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[Cfg::stage(t, i)]);
       if (g + 1 == mine) elect_commit(&sm.o_full[t]);
       if (g + kNB < mine) ok = qk(g + kNB);
     }
-    base += 2 * n;
+    base += 2 * blocks_of<DUALK>(n, t);
   }
   // the products already issued must land before the tensor memory is freed
   if (issued) {
@@ -730,17 +739,17 @@ __device__ __forceinline__ uint32_t sees(const AttendParams &p, const Item &x, i
   return bits;
 }
 
-// Whether the half block of keys from k0 on holds masked places.
-__device__ __forceinline__ bool half_masked(const AttendParams &p, const Item &x, int k0) {
+// Whether the step of keys from k0 on holds masked places.
+__device__ __forceinline__ bool step_masked(const AttendParams &p, const Item &x, int k0) {
   return p.mask != nullptr ? k0 + kHN > x.ctx : k0 + kHN - 1 > x.ctx + x.tok0;
 }
 
-// v_j that are not finite, of the masked half blocks' keys that this row sees, added to o (dims d0 .. d0 + 31).
+// v_j that are not finite, of the masked steps' keys that this row sees, added to o (dims d0 .. d0 + 31).
 template <int LAYOUT>
 __device__ __noinline__ void add_not_finite(const AttendParams &p, const Item &x, int tok, int d0, float (&o)[32]) {
   if (tok >= x.T) return;
-  for (int h0 = x.kb0 * kBN; h0 < x.kb0 * kBN + x.halves * kHN; h0 += kHN) {
-    if (!half_masked(p, x, h0)) continue;
+  for (int h0 = x.kb0 * kBN; h0 < x.kb0 * kBN + x.steps * kHN; h0 += kHN) {
+    if (!step_masked(p, x, h0)) continue;
     for (int k0 = h0; k0 < h0 + kHN; k0 += 32) {
       uint32_t bits = sees(p, x, tok, k0);
       while (bits) {
@@ -792,7 +801,6 @@ template <bool DUALK, int LAYOUT>
 __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, int warp, int lane,
                           const WaitCtl wc) {
   using Cfg = AtCfg<DUALK>;
-  constexpr int ST = Cfg::ST;
   const int t = warp >> 2, w = warp & 3, r = w * 32 + lane;
   const uint32_t lanes = (uint32_t)(32 * w) << 16;
   const uint32_t ts = tmem + lanes + kColS + 128u * t, to = tmem + lanes + kColO + 128u * t;
@@ -806,7 +814,7 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.it_empty[it & 1]);
     if (x.kb1 < 0) return;
-    const int n = x.kb1 - x.kb0, mine = halves_of<DUALK>(n, x.halves, t);
+    const int n = x.kb1 - x.kb0, mine = steps_of<DUALK>(n, x.steps, t);
     const int first_tok = x.tok0 + (DUALK ? 0 : t * (kRows >> p.g_log2));
     const int tok = first_tok + (r >> p.g_log2);
     const bool idle = first_tok + ((w * 32) >> p.g_log2) >= x.T;  // no row of this warp is one of the sequence
@@ -817,9 +825,9 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
       constexpr bool MASKED = decltype(is_masked)::value;
       const int b = g % kNB, j = DUALK ? 2 * (g / kNB) + t : g / kNB, k0 = (x.kb0 + j) * kBN + b * kHN;
       if constexpr (MASKED) {
-        const int i = base + v_load<DUALK>(n, j);
-        if (!warp_poll(&sm.kv_full[i % ST], (uint32_t)((i / ST) & 1), wc)) return false;
-        if (clean_v(sm.kv[i % ST] + b * (kHN * 128), r, &sm.poison[it & 1], it + 1))
+        const int i = base + 2 * (g / kNB) + 1;
+        if (!warp_poll(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc)) return false;
+        if (clean_v(sm.kv[Cfg::stage(t, i)] + b * (kHN * 128), r, &sm.poison[it & 1], it + 1))
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       if (!warp_poll(&sm.s_full[t][b], (sp >> b) & 1u, wc)) return false;
@@ -929,7 +937,7 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
       if (!step(std::false_type{}, g)) return;
     for (; g < mine; ++g)
       if (!step(std::true_type{}, g)) return;
-    base += 2 * n;
+    base += 2 * blocks_of<DUALK>(n, t);
 
     // output: O / l, or O, m and l as a partial
     float f0 = 1.f, f1 = 0.f;  // DUALK: factors of the two halves' O
@@ -948,7 +956,7 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
     // the last product of this half (DUALK: of both) must have been added to O
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int hi = halves_of<DUALK>(n, x.halves, i);
+      const int hi = steps_of<DUALK>(n, x.steps, i);
       od[i] += hi;
       if (hi == 0) continue;
       if ((DUALK || i == t) && !warp_poll(&sm.o_full[i], (of >> i) & 1u, wc)) return;
@@ -1025,12 +1033,16 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
 template <bool DUALK, int LAYOUT>
 __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
   using Cfg = AtCfg<DUALK>;
-  extern __shared__ uint8_t smem_dyn[];
-  AtSmem<DUALK> &sm = *reinterpret_cast<AtSmem<DUALK> *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) &
-                                                         ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_dyn[];
+  AtSmem<DUALK> &sm = *reinterpret_cast<AtSmem<DUALK> *>(smem_dyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the block's memory is full, with no room to move the tiles to a boundary
+  if (smem_u32(smem_dyn) & 1023u) {
+    if (tid == 0) atomicOr(p.status, 2);
+    return;
+  }
   if (tid == 0) {
-    for (int i = 0; i < Cfg::ST; ++i) {
+    for (int i = 0; i < Cfg::RINGS * Cfg::ST; ++i) {
       mbar_init(&sm.kv_full[i], 1);
       mbar_init(&sm.kv_empty[i], DUALK ? 1 : 2);
     }
@@ -1221,8 +1233,8 @@ cudaError_t sm_count(int *sms) {
 
 template <bool DUALK, int LAYOUT>
 cudaError_t launch_attend(const AttendParams &p, int grid, cudaStream_t st) {
-  const int smem = (int)sizeof(AtSmem<DUALK>) + 1024;
-  static_assert(sizeof(AtSmem<DUALK>) + 1024 <= kMaxDynSmem, "shared memory of the attention kernel");
+  const int smem = (int)sizeof(AtSmem<DUALK>);
+  static_assert(sizeof(AtSmem<DUALK>) <= kMaxDynSmem, "shared memory of the attention kernel");
   // the shared-memory opt-in once per device (it is a property of the kernel)
   static thread_local int attr_dev = -1;
   int dev = 0;
