@@ -161,17 +161,13 @@ struct AtSmem {
 template <int LAYOUT>
 __device__ __forceinline__ void seq_of(const AttendParams &p, int s, int &T, int &ctx, int64_t &row0, bool &bad) {
   const int64_t a = p.starts[s], b = p.starts[s + 1];
-  T = 0;
-  ctx = 0;
+  const int n = LAYOUT != kPacked ? view_len(p.view, s, p.layer) : 0;  // read at the same time
   row0 = a;
   bad = a < 0 || b < a || b > p.n_tokens;
-  if (bad || b == a) return;
-  if (LAYOUT != kPacked) {
-    ctx = view_len(p.view, s, p.layer);
-    bad = ctx < 0 || b - a > p.max_draft || b - a > p.view.max_seq_len - ctx;
-    if (bad) return;
-  }
-  T = (int)(b - a);
+  if (LAYOUT != kPacked && !bad && b > a)
+    bad = n < 0 || b - a > p.max_draft || b - a > p.view.max_seq_len - n;
+  T = bad ? 0 : (int)(b - a);
+  ctx = T > 0 ? n : 0;
 }
 
 // key blocks that tokens [.., tok_end) of a sequence see
@@ -199,7 +195,7 @@ __device__ __forceinline__ int steps_of(int n, int steps, int t) {
   return kNB * blocks_of<DUALK>(n, t) - (((n - 1) & 1) == t ? kNB * n - steps : 0);
 }
 
-// key blocks of all (KV head, tile of ROWS rows) units of a sequence
+// key blocks of a KV head's units (tiles of ROWS rows) of a sequence
 template <int ROWS>
 __device__ __forceinline__ int64_t seq_blocks(const AttendParams &p, int ctx, int T) {
   const int tpi = ROWS >> p.g_log2, tiles = (T + tpi - 1) / tpi;
@@ -209,7 +205,7 @@ __device__ __forceinline__ int64_t seq_blocks(const AttendParams &p, int ctx, in
   } else {
     for (int t = 0; t < T; t += tpi) n += key_blocks(p, ctx, T, t + tpi);
   }
-  return n * p.hkv;
+  return n;
 }
 
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
@@ -224,39 +220,39 @@ __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 template <bool DUALK>
 struct PromptCursor {
   int64_t n_items;
-  int tmax, round;
+  int tmax, round, mine;  // mine: tiles of sequence `lane` (the first 32 sequences stay in registers)
 
-  __device__ int tpi(const AttendParams &p) const { return AtCfg<DUALK>::ROWS >> p.g_log2; }
+  static __device__ __forceinline__ int tpi(const AttendParams &p) { return AtCfg<DUALK>::ROWS >> p.g_log2; }
 
-  // tiles with index >= t, over all sequences
-  __device__ int64_t from(const AttendParams &p, int t, int lane) const {
-    int64_t n = 0;
-    for (int s = lane; s < p.n_seq; s += 32) {
-      int T, ctx;
-      int64_t row0;
+  static __device__ __forceinline__ int tiles(const AttendParams &p, int s, bool &bad) {
+    int T, ctx;
+    int64_t row0;
+    seq_of<kPacked>(p, s, T, ctx, row0, bad);
+    return (T + tpi(p) - 1) / tpi(p);
+  }
+
+  // tiles with index >= t, over all sequences (their number fits 31 bits, as the tokens' does)
+  __device__ __forceinline__ int from(const AttendParams &p, int t, int lane) const {
+    int n = max(0, mine - t);
+    for (int s = 32 + lane; s < p.n_seq; s += 32) {
       bool bad;
-      seq_of<kPacked>(p, s, T, ctx, row0, bad);
-      n += max(0, (T + tpi(p) - 1) / tpi(p) - t);
+      n += max(0, tiles(p, s, bad) - t);
     }
-    return warp_sum(n);
+    return __reduce_add_sync(kFull, n);
   }
 
   __device__ void init(const AttendParams &p, int lane) {
-    int most = 0;
     bool any_bad = false;
-    for (int s = lane; s < p.n_seq; s += 32) {
-      int T, ctx;
-      int64_t row0;
+    mine = lane < p.n_seq ? tiles(p, lane, any_bad) : 0;
+    int most = mine;
+    for (int s = 32 + lane; s < p.n_seq; s += 32) {
       bool bad;
-      seq_of<kPacked>(p, s, T, ctx, row0, bad);
+      most = max(most, tiles(p, s, bad));
       any_bad = any_bad || bad;
-      most = max(most, (T + tpi(p) - 1) / tpi(p));
     }
     if (any_bad && blockIdx.x == 0) atomicOr(p.status, 1);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(kFull, most, o));
-    tmax = most;
-    n_items = from(p, 0, lane) * p.hkv;
+    tmax = __reduce_max_sync(kFull, most);
+    n_items = (int64_t)from(p, 0, lane) * p.hkv;
     round = 0;
   }
 
@@ -265,25 +261,29 @@ struct PromptCursor {
     const int64_t k = round * grid + ((round & 1) ? grid - 1 - b : b);
     ++round;
     if (k >= n_items) return false;  // later rounds begin behind k
-    const int64_t pos = k / p.hkv;
+    const int pos = (int)(k / p.hkv);
     x.h = (int)(k % p.hkv);
     int lo = 0, hi = tmax - 1;  // the largest t with from(t) > pos
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (from(p, mid, lane) > pos) lo = mid; else hi = mid - 1;
+    if (p.n_seq == 1) {
+      lo = tmax - 1 - pos;
+    } else {
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (from(p, mid, lane) > pos) lo = mid; else hi = mid - 1;
+      }
     }
-    int64_t rem = pos - from(p, lo + 1, lane);
-    x.s = -1;
+    int rem = p.n_seq == 1 ? 0 : pos - from(p, lo + 1, lane);
+    x.s = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-      const int s = s0 + lane;
-      int T = 0, ctx;
-      int64_t row0;
-      bool bad;
-      if (s < p.n_seq) seq_of<kPacked>(p, s, T, ctx, row0, bad);
-      const uint32_t has = __ballot_sync(kFull, (T + tpi(p) - 1) / tpi(p) > lo);
+      int t = mine;
+      if (s0 > 0) {
+        bool bad;
+        t = s0 + lane < p.n_seq ? tiles(p, s0 + lane, bad) : 0;
+      }
+      const uint32_t has = __ballot_sync(kFull, t > lo);
       const int cnt = __popc(has);
       if (rem < cnt) {
-        x.s = s0 + __fns(has, 0, (int)rem + 1);
+        x.s = s0 + __fns(has, 0, rem + 1);
         break;
       }
       rem -= cnt;
@@ -299,48 +299,68 @@ struct PromptCursor {
   }
 };
 
-// Drafted tokens: the key blocks of all units (sequence, KV head, tile of
-// rows) in one line, cut into one piece of equal length per CTA.  A unit that
-// lies in several pieces is put together from partials by combine_kernel.
+// Drafted tokens: the key blocks of all units (sequence, KV head, tile of rows)
+// in one line, cut into one piece of equal length per CTA.  A unit that lies in
+// several pieces is put together from partials by combine_kernel.
+// Paged caches whose rows lie head by head inside a page: one line for each KV
+// head, cut into grid / hkv pieces, and neighbouring CTAs take the same piece
+// for all heads, so that the pages are read whole at about the same time (64
+// sequences of 2048 rows, 8 KV heads, 16-row pages: MEASURED).
+struct Lines {
+  int heads, cuts, step;  // KV heads in a line, pieces of a line, CTAs between two pieces
+  // CTA of piece c of head h's line
+  __host__ __device__ __forceinline__ int cta(int c, int h) const { return c * step + (step > 1 ? h : 0); }
+};
+
+template <int LAYOUT>
+__host__ __device__ __forceinline__ Lines lines_of(int hkv, int grid) {
+  if (LAYOUT == TRIA_LAYOUT_PAGED && hkv > 1 && grid >= hkv) return {1, grid / hkv, hkv};
+  return {hkv, grid, 1};
+}
+
 template <bool DUALK, int LAYOUT>
 struct TreeCursor {
   int64_t pos, end, ub;  // blocks of this CTA still to do; where the unit begins
-  int s, h, tok0, T, ctx, pieces;
+  int s, h, tok0, T, ctx, pieces, heads;
   int64_t row0;
 
-  static __device__ int64_t total(const AttendParams &p, int lane, bool &any_bad) {
-    int64_t n = 0;
-    any_bad = false;
-    for (int s = lane; s < p.n_seq; s += 32) {
-      int T, ctx;
-      int64_t row0;
-      bool bad;
-      seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
-      any_bad = any_bad || bad;
-      n += seq_blocks<AtCfg<DUALK>::ROWS>(p, ctx, T);
-    }
-    return warp_sum(n);
+  static __device__ __forceinline__ int tpi(const AttendParams &p) { return AtCfg<DUALK>::ROWS >> p.g_log2; }
+
+  // blocks of sequence s in one head's line
+  static __device__ __forceinline__ int64_t blocks(const AttendParams &p, int s, bool &bad) {
+    int T, ctx;
+    int64_t row0;
+    seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
+    return seq_blocks<AtCfg<DUALK>::ROWS>(p, ctx, T);
   }
 
   __device__ void init(const AttendParams &p, int lane) {
-    bool any_bad;
-    const int64_t all = total(p, lane, any_bad);
+    const Lines li = lines_of<LAYOUT>(p.hkv, gridDim.x);
+    heads = li.heads;
+    // the first 32 sequences stay in registers
+    bool any_bad = false;
+    const int64_t c0 = lane < p.n_seq ? blocks(p, lane, any_bad) * heads : 0;
+    int64_t all = c0;
+    for (int s = 32 + lane; s < p.n_seq; s += 32) {
+      bool bad;
+      all += blocks(p, s, bad) * heads;
+      any_bad = any_bad || bad;
+    }
+    all = warp_sum(all);
     if (any_bad && blockIdx.x == 0) atomicOr(p.status, 1);
-    const int64_t w = (all + gridDim.x - 1) / gridDim.x;
-    pos = blockIdx.x * w;
-    end = min(all, pos + w);
+    const int64_t w = (all + li.cuts - 1) / li.cuts;
+    const int cut = blockIdx.x / li.step;
+    pos = cut * w;
+    end = cut < li.cuts ? min(all, pos + w) : 0;
     pieces = 0;
     if (pos >= end) return;
     // the sequence that holds block `pos`
     int64_t before = 0;
     for (int s0 = 0;; s0 += 32) {
-      int64_t c = 0;
-      if (s0 + lane < p.n_seq) {
-        int t, x;
-        int64_t r;
+      int64_t c = c0;
+      if (s0 > 0) {
         bool bad;
-        seq_of<LAYOUT>(p, s0 + lane, t, x, r, bad);
-        c = seq_blocks<AtCfg<DUALK>::ROWS>(p, x, t);
+        c = s0 + lane < p.n_seq ? blocks(p, s0 + lane, bad) * heads : 0;
       }
       int64_t incl = c;
 #pragma unroll
@@ -357,6 +377,7 @@ struct TreeCursor {
       }
       before += __shfl_sync(kFull, incl, 31);
     }
+    h = heads > 1 ? 0 : blockIdx.x % li.step;
     load(p);
     while (ub + unit(p) <= pos) step(p);
   }
@@ -364,16 +385,16 @@ struct TreeCursor {
   __device__ void load(const AttendParams &p) {
     bool bad;
     seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
-    h = tok0 = 0;
+    if (heads > 1) h = 0;
+    tok0 = 0;
   }
-  __device__ int tpi(const AttendParams &p) const { return AtCfg<DUALK>::ROWS >> p.g_log2; }
   __device__ int unit(const AttendParams &p) const { return key_blocks(p, ctx, T, tok0 + tpi(p)); }
   __device__ void step(const AttendParams &p) {
     ub += unit(p);
     tok0 += tpi(p);
     if (tok0 < T) return;
     tok0 = 0;
-    if (++h < p.hkv) return;
+    if (heads > 1 && ++h < heads) return;
     do {
       ++s;
       load(p);
@@ -1065,6 +1086,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == kLoadWarp && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &p.qmap : lane == 1 ? &p.kmap : &p.vmap) : "memory");
   if (warp == kIssueWarp) tmem_alloc(&sm.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
@@ -1106,38 +1130,40 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
   const int tpi = ROWS >> p.g_log2, tok0 = blockIdx.y * tpi;
-  int T, ctx;
-  int64_t row0;
-  bool bad;
-  seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
-  if (tok0 >= T) return;
-  int64_t all = 0, before = 0;  // key blocks of every sequence, of those before s
+  const Lines li = lines_of<LAYOUT>(p.hkv, grid);
+  int64_t all = 0, before = 0;  // key blocks of every sequence in a line, of those before s
   for (int i = lane; i < p.n_seq; i += 32) {
-    int t, c;
-    int64_t r;
-    seq_of<LAYOUT>(p, i, t, c, r, bad);
-    const int64_t n = seq_blocks<ROWS>(p, c, t);
+    bool bad;
+    const int64_t n = TreeCursor<DUALK, LAYOUT>::blocks(p, i, bad) * li.heads;
     all += n;
     if (i < s) before += n;
   }
   all = warp_sum(all);
   before = warp_sum(before);
-  const int64_t w = (all + grid - 1) / grid;
-  int64_t ub = before + h * (seq_blocks<ROWS>(p, ctx, T) / p.hkv);
+  int T, ctx;
+  int64_t row0;
+  bool bad;
+  seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
+  // up to here this kernel may run beside the end of attend_kernel
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tok0 >= T) return;
+  const int64_t w = (all + li.cuts - 1) / li.cuts;
+  int64_t ub = before;
+  if (li.heads > 1) ub += h * seq_blocks<ROWS>(p, ctx, T);
   for (int t = 0; t < tok0; t += tpi) ub += key_blocks(p, ctx, T, t + tpi);
   const int nb = key_blocks(p, ctx, T, tok0 + tpi);
   const int c0 = (int)(ub / w), c1 = (int)((ub + nb - 1) / w);
   if (c0 == c1) return;  // one CTA did it all and wrote the output
   const int rows = min(T - tok0, tpi) << p.g_log2;
   for (int r = blockIdx.z * kCombineWarps + warp; r < rows; r += gridDim.z * kCombineWarps) {
-    auto at = [&](int c) { return (int64_t)(2 * c + (c == c0 && ub > c0 * w ? 1 : 0)) * ROWS + r; };
+    auto at = [&](int c) { return (int64_t)(2 * li.cta(c, h) + (c == c0 && ub > c0 * w ? 1 : 0)) * ROWS + r; };
     float M = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.part_ml + at(c) * 2));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int c = c0; c <= c1; ++c) {
       const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c) * 2));
       const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(c) * 128) + lane);
@@ -1286,8 +1312,18 @@ cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t
   int64_t z = (2 * 148 + units - 1) / units;
   if (z > (rows + kCombineWarps - 1) / kCombineWarps) z = (rows + kCombineWarps - 1) / kCombineWarps;
   const dim3 grid((unsigned)(p.n_seq * p.hkv), (unsigned)sh.tiles, (unsigned)z);
-  combine_kernel<DUALK, LAYOUT><<<grid, 32 * kCombineWarps, 0, st>>>(p, sh.grid);
-  return cudaGetLastError();
+  // launched while attend_kernel still runs: what it reads of the call's inputs
+  // it reads then, and it waits for the partials
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<DUALK, LAYOUT>, p, sh.grid);
 }
 
 }  // namespace
