@@ -15,14 +15,20 @@
 //   DUALK: one tile of rows, its even and odd key blocks (at most 128 rows:
 //          both halves of the SM stay busy although there is one tile).
 // Roles (one CTA per SM, persistent):
-//   warps 0-3, 4-7  softmax of tile (or half) 0 and 1, one thread per row:
+//   warps 0-3, 4-7  softmax of tile (or key half) 0 and 1, one thread per row:
 //                   S from tensor memory, running maximum and sum in fp32,
 //                   P as bf16 back over S, the output at the end;
-//   warp 8          issues tcgen05.mma (one elected lane): S = Q K^T (both in shared
-//                   memory), O += P V (P in tensor memory, V as it lies,
-//                   MN-major); while one tile's softmax runs, the other's
-//                   products do;
-//   warp 9          items of work, and TMA loads of Q and the K/V ring.
+//   warps 8, 10     issue tcgen05.mma for half 0 and 1 (one elected lane):
+//                   S = Q K^T (both in shared memory), O += P V (P in tensor
+//                   memory, V as it lies, MN-major);
+//   warp 9          items of work, and TMA loads of Q and the K tiles;
+//   warp 11         TMA loads of the V tiles.
+// A step is 64 keys, and each half has two buffers of S, so the product of the
+// next step is ready while the softmax of this one runs: with one 128-key
+// buffer the chain product, softmax, product set the pace (8448-token prompt,
+// 32 query and 8 KV heads: 597 us against 540).  What bounds it now: the
+// products alone take 449 us of that (Q K^T in steps of 64 keys is bound by
+// shared memory), the exponentials, conversions and maxima alone 433 us.
 // P is rounded to bf16: the second product needs 16-bit operands, the output
 // is rounded to bf16 anyway, and l sums the unrounded weights.
 //
@@ -82,10 +88,11 @@ __device__ __forceinline__ bool warp_poll(uint64_t *bar, uint32_t parity, const 
 constexpr int kBN = 128;                       // keys per block (a ring stage of K or V)
 constexpr int kHN = 64;                        // keys per step (a product and its softmax)
 constexpr int kNB = kBN / kHN;                 // steps per block, and buffers of S in tensor memory
+static_assert(kNB == 2, "mma_role's order of releases");
 constexpr int kTile = 2 * kHalfBlock;          // bytes of 128 rows x 128 bf16
 constexpr int kSoftWarps = 8;
-constexpr int kIssueWarp = 8, kLoadWarp = 9;   // issue: 8 and 10
-constexpr int kAtThreads = 384;                 // the third warpgroup holds the two single-warp roles
+constexpr int kIssueWarp = 8, kLoadWarp = 9;   // issue: 8 and 10; loads: 9 (items, Q, K) and 11 (V)
+constexpr int kAtThreads = 384;                 // the third warpgroup holds the four single-warp roles
 // Registers a thread: the kernel is launched with 168 (65536 / 384, rounded
 // down to 8); the softmax groups hold a row of S and raise theirs, the third
 // group gives up what they take (2 x 208 + 88 = 3 x 168).
@@ -430,65 +437,98 @@ __device__ __forceinline__ uint64_t normal_policy() {
   return pol;
 }
 
+// The K or the V tiles of the items, by one warp each: a tile of a paged cache
+// with small pages is up to 32 boxes, and one warp for both fell behind (64
+// paged sequences of 2048 rows: 141 us against 116).  A stage passes between
+// the two warps; its phases stay apart because the stages of a ring come free in
+// the order of the loads (mma_role), so when load i - 2 found its stage free,
+// every phase before the one load i waits for is over.
+template <bool DUALK, int LAYOUT, bool IS_V>
+struct TileLoads {
+  using Cfg = AtCfg<DUALK>;
+  uint64_t pol;
+  int base[Cfg::RINGS];  // loads of each ring before the item
+  int done[Cfg::RINGS];  // this warp's last load of each ring, or -1
+
+  __device__ TileLoads() {
+    // drafted rows read the cache once; prompts read their keys again for later tiles
+    pol = LAYOUT != kPacked && DUALK ? evict_first_policy() : normal_policy();
+    for (int t = 0; t < Cfg::RINGS; ++t) {
+      base[t] = 0;
+      done[t] = -1;
+    }
+  }
+
+  // all tiles of an item; false when a wait ran out
+  __device__ bool item(const AttendParams &p, AtSmem<DUALK> &sm, const Item &x, int lane, const WaitCtl &wc) {
+    const CUtensorMap *map = IS_V ? &p.vmap : &p.kmap;
+    const int n = x.kb1 - x.kb0, bs = p.view.block_size, at = lane >> 1, half = lane & 1;
+    auto page = [&](int j) {  // this lane's block id of key block j
+      const int t = (x.kb0 + j) * kBN + at * bs;
+      return LAYOUT == TRIA_LAYOUT_PAGED && j < n && at < kBN / bs && t < x.ctx + x.T
+                 ? __ldg(p.view.block_table + (int64_t)x.s * p.view.max_blocks + t / bs)
+                 : 0;
+    };
+    int blk = page(0);
+    for (int j = 0; j < n; ++j) {
+      const int t = DUALK ? j & 1 : 0, i = base[t] + 2 * (DUALK ? j >> 1 : j) + (IS_V ? 1 : 0);
+      const int stage = Cfg::stage(t, i), slot0 = (x.kb0 + j) * kBN;
+      if (i >= Cfg::ST) {
+        bool free = true;
+        if (lane == 0) free = poll(&sm.kv_empty[stage], Cfg::phase(i - Cfg::ST), wc);
+        if (!__shfl_sync(kFull, free ? 1 : 0, 0)) return false;
+      }
+      const uint32_t dst = smem_u32(&sm.kv[stage][0]);
+      if (LAYOUT != TRIA_LAYOUT_PAGED) {
+        if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[stage], kTile);
+        __syncwarp();
+        if (lane < 2) {
+          if (LAYOUT == kPacked)
+            tma_load_4d(dst + lane * kHalfBlock, map, lane * 64, (int)x.row0 + slot0, x.h, 0, &sm.kv_full[stage], pol);
+          else
+            tma_load_4d(dst + lane * kHalfBlock, map, lane * 64, slot0, x.h, x.s, &sm.kv_full[stage], pol);
+        }
+      } else {
+        // one box per page and 64-dim half; pages behind the last row stay unread
+        // (what the stage holds there is masked)
+        const bool valid = at < kBN / bs && slot0 + at * bs < x.ctx + x.T;
+        const int boxes = __popc(__ballot_sync(kFull, valid)), now = blk;
+        blk = page(j + 1);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[stage], (uint32_t)(boxes * bs * 128));
+        __syncwarp();
+        if (valid)
+          tma_load_4d(dst + half * kHalfBlock + at * bs * 128, map, half * 64, x.h, 0, now, &sm.kv_full[stage], pol);
+      }
+      done[t] = i;
+    }
+    for (int t = 0; t < Cfg::RINGS; ++t) base[t] += 2 * blocks_of<DUALK>(n, t);
+    return true;
+  }
+
+  // aborted: this warp's loads still in flight must land before the block exits
+  // (of those ST and more back, the stage was used again only after they had)
+  __device__ void drain(AtSmem<DUALK> &sm, const WaitCtl &wc) {
+    for (int t = 0; t < Cfg::RINGS; ++t)
+      for (int i = max(IS_V ? 1 : 0, done[t] - 2 * (Cfg::ST / 2)); i <= done[t]; i += 2)
+        mbar_drain(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc.status);
+  }
+};
+
+// Items of work for everyone, Q and K.
 template <bool DUALK, int LAYOUT, class Cursor>
 __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, const WaitCtl wc) {
   using Cfg = AtCfg<DUALK>;
-  constexpr int ST = Cfg::ST;
-  // drafted rows read the cache once; prompts read their keys again for later tiles
-  const uint64_t pol = LAYOUT != kPacked && DUALK ? evict_first_policy() : normal_policy();
   const uint64_t qpol = normal_policy();
+  TileLoads<DUALK, LAYOUT, false> keys;
   Cursor cur;
   cur.init(p, lane);
-  int it = 0;
+  int it = 0, q_loads = 0;
   bool ok = true;
   Item x{};
   auto wait = [&](uint64_t *bar, int phase) {
     bool good = true;
     if (lane == 0) good = poll(bar, (uint32_t)(phase & 1), wc);
     return __shfl_sync(kFull, good ? 1 : 0, 0) != 0;
-  };
-  int next_blk = -1, next_j = -1;
-  auto table = [&](int j) {  // this lane's block id of key block j of the item
-    const int bs = p.view.block_size, t = (x.kb0 + j) * kBN + (lane >> 1) * bs;
-    return (lane >> 1) < kBN / bs && t < x.ctx + x.T
-               ? __ldg(p.view.block_table + (int64_t)x.s * p.view.max_blocks + t / bs)
-               : 0;
-  };
-  int li[Cfg::RINGS] = {};  // loads of each ring so far
-  // K or V of key block j of the item
-  auto load = [&](bool is_v, int j, int n) -> bool {
-    const int t = DUALK ? j & 1 : 0, i = li[DUALK ? t : 0], stage = Cfg::stage(t, i);
-    if (i >= ST && !wait(&sm.kv_empty[stage], i / ST - 1)) return false;
-    const CUtensorMap *map = is_v ? &p.vmap : &p.kmap;
-    const uint32_t dst = smem_u32(&sm.kv[stage][0]);
-    const int slot0 = (x.kb0 + j) * kBN;
-    if (LAYOUT != TRIA_LAYOUT_PAGED) {
-      if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[stage], kTile);
-      __syncwarp();
-      if (lane < 2) {
-        if (LAYOUT == kPacked)
-          tma_load_4d(dst + lane * kHalfBlock, map, lane * 64, (int)x.row0 + slot0, x.h, 0, &sm.kv_full[stage], pol);
-        else
-          tma_load_4d(dst + lane * kHalfBlock, map, lane * 64, slot0, x.h, x.s, &sm.kv_full[stage], pol);
-      }
-    } else {
-      // one box per page and 64-dim half; pages behind the last row stay unread
-      // (what the stage holds there is masked)
-      const int bs = p.view.block_size, at = lane >> 1, half = lane & 1;
-      const bool valid = at < kBN / bs && slot0 + at * bs < x.ctx + x.T;
-      const int blk = !is_v && next_j == j ? next_blk : table(j);
-      const int boxes = __popc(__ballot_sync(kFull, valid));
-      if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[stage], (uint32_t)(boxes * bs * 128));
-      __syncwarp();
-      if (valid)
-        tma_load_4d(dst + half * kHalfBlock + at * bs * 128, map, half * 64, x.h, 0, blk, &sm.kv_full[stage], pol);
-      if (!is_v) {
-        next_j = j + 1 < n ? j + 1 : -1;
-        if (next_j >= 0) next_blk = table(next_j);
-      }
-    }
-    ++li[DUALK ? t : 0];
-    return true;
   };
   for (;;) {
     const bool more = cur.next(p, lane, x);
@@ -501,7 +541,6 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
     }
     ++it;
     if (!more) break;
-    next_j = -1;
     if (it > 1 && !(ok = wait(&sm.q_empty, it - 2))) break;
     if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, Cfg::QT * kTile);
     __syncwarp();
@@ -510,24 +549,30 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
       tma_load_4d(smem_u32(&sm.q[t][half * kHalfBlock]), &p.qmap, half * 64, x.h << p.g_log2,
                   (int)x.row0 + x.tok0 + t * (kRows >> p.g_log2), 0, &sm.q_full, qpol);
     }
-    const int n = x.kb1 - x.kb0;
-    // in the order in which mma_role uses them
-    if (DUALK) {
-      for (int j = 0; ok && j < n; j += 2)
-        ok = load(false, j, n) && (j + 1 == n || load(false, j + 1, n)) && load(true, j, n) &&
-             (j + 1 == n || load(true, j + 1, n));
-    } else {
-      for (int j = 0; ok && j < n; ++j) ok = load(false, j, n) && load(true, j, n);
-    }
-    if (!ok) break;
+    ++q_loads;
+    if (!(ok = keys.item(p, sm, x, lane, wc))) break;
   }
   if (!ok && lane == 0) {
-    // aborted: loads still in flight must land before the block exits
-    for (int t = 0; t < Cfg::RINGS; ++t)
-      for (int i = li[t] > ST ? li[t] - ST : 0; i < li[t]; ++i)
-        mbar_drain(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc.status);
-    if (it > 0) mbar_drain(&sm.q_full, (it - 1) & 1, wc.status);
+    keys.drain(sm, wc);
+    if (q_loads > 0) mbar_drain(&sm.q_full, (q_loads - 1) & 1, wc.status);
   }
+  __syncwarp();
+}
+
+template <bool DUALK, int LAYOUT>
+__device__ void value_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, const WaitCtl wc) {
+  TileLoads<DUALK, LAYOUT, true> values;
+  bool ok = true;
+  for (int it = 0; ok; ++it) {
+    if (!(ok = warp_poll(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc))) break;
+    const Item x = sm.item[it & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.it_empty[it & 1]);
+    if (x.kb1 < 0) break;
+    ok = values.item(p, sm, x, lane, wc);
+  }
+  if (!ok && lane == 0) values.drain(sm, wc);
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -613,13 +658,16 @@ __device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem
     const int mine = steps_of<DUALK>(n, steps, t);
     if (mine == 0 && lane == 0) mbar_arrive(&sm.q_empty);
     auto kv_wait = [&](int i) { return warp_poll(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc); };
-    // S of half block g into buffer g & 1; its last half releases K
+    // S of step g into its buffer.  K is released behind its last step, but never
+    // before V of the block before it (the loads count on stages coming free in
+    // the order of their use): a block with one step leaves that to the product
+    // of the step before it.
     auto qk = [&](int g) {
       const int i = base + 2 * (g / kNB), b = g % kNB;
       if (b == 0 && !kv_wait(i)) return false;
       mma_qk(s_col + 64u * b, q_at, k_at + (uint32_t)(Cfg::stage(t, i) * (kTile >> 4)) + b * kHalfRows, kIdescS);
       elect_commit(&sm.s_full[t][b]);
-      if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[Cfg::stage(t, i)]);
+      if (b == kNB - 1 || mine == 1) elect_commit(&sm.kv_empty[Cfg::stage(t, i)]);
       if (g + 1 == mine) elect_commit(&sm.q_empty);
       issued = true;
       return true;
@@ -634,6 +682,7 @@ __device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem
       mma_pv(o_col, s_col + 64u * b, v_at + (uint32_t)(Cfg::stage(t, i) * (kTile >> 4)) + b * kHalfRows, kIdescO, g > 0 ? 1u : 0u);
       if (kNB > 1) elect_commit(&sm.o_done[t]);
       if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[Cfg::stage(t, i)]);
+      if (b == kNB - 1 && g + 2 == mine) elect_commit(&sm.kv_empty[Cfg::stage(t, i + 1)]);
       if (g + 1 == mine) elect_commit(&sm.o_full[t]);
       if (g + kNB < mine) ok = qk(g + kNB);
     }
@@ -1078,7 +1127,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       mbar_init(&sm.o_full[i], 1);
       mbar_init(&sm.drain[i], 1);
       mbar_init(&sm.it_full[i], 1);
-      mbar_init(&sm.it_empty[i], kSoftWarps + 2);
+      mbar_init(&sm.it_empty[i], kSoftWarps + 3);
       sm.poison[i] = 0;
     }
     mbar_init(&sm.ml_full, kSoftWarps);
@@ -1105,7 +1154,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
         load_role<DUALK, LAYOUT, PromptCursor<DUALK>>(p, sm, lane, wc);
       else
         load_role<DUALK, LAYOUT, TreeCursor<DUALK, LAYOUT>>(p, sm, lane, wc);
-    } else if (warp == kIssueWarp || warp == kIssueWarp + 2) {
+    } else if (warp == kLoadWarp + 2) {
+      value_role<DUALK, LAYOUT>(p, sm, lane, wc);
+    } else {
       mma_role<DUALK>(p, sm, tmem, (warp - kIssueWarp) >> 1, lane, wc);
     }
   }

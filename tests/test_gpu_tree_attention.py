@@ -117,6 +117,25 @@ def test_long_context_split_over_many_blocks():
         st.free()
 
 
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("n_draft", [5, 40])
+def test_many_key_blocks_and_several_units_for_each_processor(block, n_draft):
+    # odd numbers of 64-key steps, units that begin and end inside a piece; again and again the same bits
+    st = Store(T, 1, 32, 8, [20011, 6450, 13000], 20064, block=block, seed=15)
+    try:
+        d = Drafts(st, 32, [n_draft, 3, n_draft], seed=15)
+        d.run()
+        a, al = d.out.clone(), d.lse.clone()
+        d.check(heads=[0, 13, 31])
+        for _ in range(30):
+            d.run()
+        torch.cuda.synchronize()
+        assert torch.equal(a, d.out) and torch.equal(al, d.lse)
+        assert T.tria_read_device_status(d.ws) == 0
+    finally:
+        st.free()
+
+
 def test_many_paged_sequences_of_different_lengths():
     lens = [(173 * i) % 1999 for i in range(40)]
     drafts = [(5 * i) % 13 for i in range(40)]
