@@ -109,6 +109,15 @@ constexpr float kSlack = 8.f;
 // special-function unit.
 constexpr int kFmaOf8 = 1;
 
+// A unit (sequence, KV head, tile of rows) whose key blocks several CTAs share,
+// written down by the CTA that has its first block: its rows, the slot of the
+// first partial, and those of the others.
+struct Shared {
+  int64_t row0;          // first token's row in the output
+  int h, rows;           // rows: 0 when no unit begins in this CTA and goes on in the next
+  int first, next, step, count;  // slots: first, then next, next + step, ... (count of them)
+};
+
 struct AttendParams {
   CUtensorMap qmap, kmap, vmap;
   const uint16_t *v;
@@ -124,6 +133,7 @@ struct AttendParams {
   uint16_t *out;
   float *lse;
   float *part_o, *part_ml;                     // [2 grid][rows][128], [2 grid][rows][2]
+  Shared *shared;                              // [grid]
   int32_t *status;
 };
 
@@ -304,6 +314,8 @@ struct PromptCursor {
     x.slot = -1;
     return true;
   }
+
+  __device__ void finish(const AttendParams &p) const {}
 };
 
 // Drafted tokens: the key blocks of all units (sequence, KV head, tile of rows)
@@ -329,7 +341,8 @@ template <bool DUALK, int LAYOUT>
 struct TreeCursor {
   int64_t pos, end, ub;  // blocks of this CTA still to do; where the unit begins
   int s, h, tok0, T, ctx, pieces, heads;
-  int64_t row0;
+  int64_t row0, w;       // w: blocks of a piece
+  Shared goes_on;        // the unit that begins here and goes on in the next CTA
 
   static __device__ __forceinline__ int tpi(const AttendParams &p) { return AtCfg<DUALK>::ROWS >> p.g_log2; }
 
@@ -355,7 +368,8 @@ struct TreeCursor {
     }
     all = warp_sum(all);
     if (any_bad && blockIdx.x == 0) atomicOr(p.status, 1);
-    const int64_t w = (all + li.cuts - 1) / li.cuts;
+    w = (all + li.cuts - 1) / li.cuts;
+    goes_on.rows = 0;
     const int cut = blockIdx.x / li.step;
     pos = cut * w;
     end = cut < li.cuts ? min(all, pos + w) : 0;
@@ -421,11 +435,23 @@ struct TreeCursor {
     x.kb1 = (int)(min(end, ub + nb) - ub);
     x.steps = item_steps(p, x, tok0 + tpi(p));
     x.slot = x.kb1 - x.kb0 == nb ? -1 : 2 * (int)blockIdx.x + (pieces > 0 ? 1 : 0);
+    if (x.kb0 == 0 && x.kb1 < nb) {
+      const int step = lines_of<LAYOUT>(p.hkv, gridDim.x).step;
+      goes_on.row0 = row0 + tok0;
+      goes_on.h = h;
+      goes_on.rows = min(T - tok0, tpi(p)) << p.g_log2;
+      goes_on.first = x.slot;
+      goes_on.next = 2 * ((int)blockIdx.x + step);  // the next CTA's first piece
+      goes_on.step = 2 * step;
+      goes_on.count = (int)((nb - x.kb1 + w - 1) / w);
+    }
     pos = ub + x.kb1;
     ++pieces;
     if (pos < end) step(p);
     return true;
   }
+
+  __device__ void finish(const AttendParams &p) const { p.shared[blockIdx.x] = goes_on; }
 };
 
 // ---------------------------------------------------------------------------
@@ -540,7 +566,10 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
       mbar_arrive(&sm.it_full[slot]);
     }
     ++it;
-    if (!more) break;
+    if (!more) {
+      if (lane == 0) cur.finish(p);
+      break;
+    }
     if (it > 1 && !(ok = wait(&sm.q_empty, it - 2))) break;
     if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, Cfg::QT * kTile);
     __syncwarp();
@@ -1169,64 +1198,76 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------------------
-// Partials of a unit (sequence, KV head, tile of rows) that several CTAs
-// worked on, put together: out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-// One warp per row, a lane holds 4 dims.
+// Partials of a unit that several CTAs worked on, put together: out = sum_c
+// 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.  One warp per row, a lane holds 4
+// dims.  Latency bounds it: the unit's record, then its partials all at once.
 // ---------------------------------------------------------------------------
 constexpr int kCombineWarps = 8;
+constexpr int kBatch = 10;  // partials in flight per row
 
-template <bool DUALK, int LAYOUT>
-__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const __grid_constant__ AttendParams p, int grid) {
-  constexpr int ROWS = AtCfg<DUALK>::ROWS;
+template <int ROWS>
+__global__ void __launch_bounds__(32 * kCombineWarps, 3) combine_kernel(const __grid_constant__ AttendParams p, int grid) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // started beside the end of attend_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int s = blockIdx.x / p.hkv, h = blockIdx.x % p.hkv;
-  const int tpi = ROWS >> p.g_log2, tok0 = blockIdx.y * tpi;
-  const Lines li = lines_of<LAYOUT>(p.hkv, grid);
-  int64_t all = 0, before = 0;  // key blocks of every sequence in a line, of those before s
-  for (int i = lane; i < p.n_seq; i += 32) {
-    bool bad;
-    const int64_t n = TreeCursor<DUALK, LAYOUT>::blocks(p, i, bad) * li.heads;
-    all += n;
-    if (i < s) before += n;
-  }
-  all = warp_sum(all);
-  before = warp_sum(before);
-  int T, ctx;
-  int64_t row0;
-  bool bad;
-  seq_of<LAYOUT>(p, s, T, ctx, row0, bad);
-  // up to here this kernel may run beside the end of attend_kernel
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tok0 >= T) return;
-  const int64_t w = (all + li.cuts - 1) / li.cuts;
-  int64_t ub = before;
-  if (li.heads > 1) ub += h * seq_blocks<ROWS>(p, ctx, T);
-  for (int t = 0; t < tok0; t += tpi) ub += key_blocks(p, ctx, T, t + tpi);
-  const int nb = key_blocks(p, ctx, T, tok0 + tpi);
-  const int c0 = (int)(ub / w), c1 = (int)((ub + nb - 1) / w);
-  if (c0 == c1) return;  // one CTA did it all and wrote the output
-  const int rows = min(T - tok0, tpi) << p.g_log2;
-  for (int r = blockIdx.z * kCombineWarps + warp; r < rows; r += gridDim.z * kCombineWarps) {
-    auto at = [&](int c) { return (int64_t)(2 * li.cta(c, h) + (c == c0 && ub > c0 * w ? 1 : 0)) * ROWS + r; };
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.part_ml + at(c) * 2));
+  // the blockIdx.x-th of the CTAs in which a shared unit begins
+  int cta = -1;
+  for (int c0 = 0, before = 0; c0 < grid && cta < 0; c0 += 32 * 5) {
+    int rows[5];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float L = 0.f;
+    for (int i = 0; i < 5; ++i) {
+      const int c = c0 + 32 * i + lane;
+      rows[i] = c < grid ? __ldcg(&p.shared[c].rows) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const uint32_t has = __ballot_sync(kFull, rows[i] > 0);
+      const int nth = (int)blockIdx.x - before;
+      if (cta < 0 && nth < __popc(has)) cta = c0 + 32 * i + __fns(has, 0, nth + 1);
+      before += __popc(has);
+    }
+  }
+  if (cta < 0) return;
+  const Shared u = p.shared[cta];
+  for (int r = blockIdx.y * kCombineWarps + warp; r < u.rows; r += gridDim.y * kCombineWarps) {
+    // partial c: 0 is the first CTA's
+    auto at = [&](int c) { return (int64_t)(c == 0 ? u.first : u.next + (c - 1) * u.step) * ROWS + r; };
+    float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(c) * 2));
-      const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(c) * 128) + lane);
-      const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-      L = fmaf(a, ml.y, L);
-      acc.x = fmaf(a, o.x, acc.x);
-      acc.y = fmaf(a, o.y, acc.y);
-      acc.z = fmaf(a, o.z, acc.z);
-      acc.w = fmaf(a, o.w, acc.w);
+    for (int b = 0; b <= u.count; b += kBatch) {
+      // the batch's partials and their m and l are on their way at the same time
+      const int n = min(kBatch, u.count + 1 - b);
+      float4 o[kBatch];
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c)
+        if (c < n) o[c] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(b + c) * 128) + lane);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(b + lane) * 2));
+      float top = fmaxf(M, ml.x);
+#pragma unroll
+      for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
+      const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - top), back = M == -INFINITY ? 0.f : ex2(M - top);
+      M = top;
+      float l = a * ml.y;
+#pragma unroll
+      for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
+      L = fmaf(L, back, l);
+      acc.x *= back;
+      acc.y *= back;
+      acc.z *= back;
+      acc.w *= back;
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const float f = __shfl_sync(kFull, a, c);
+        if (c < n) {
+          acc.x = fmaf(f, o[c].x, acc.x);
+          acc.y = fmaf(f, o[c].y, acc.y);
+          acc.z = fmaf(f, o[c].z, acc.z);
+          acc.w = fmaf(f, o[c].w, acc.w);
+        }
+      }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t orow = (row0 + tok0 + (r >> p.g_log2)) * p.hq + ((int64_t)h << p.g_log2) + (r & (p.g - 1));
+    const int64_t orow = (u.row0 + (r >> p.g_log2)) * p.hq + ((int64_t)u.h << p.g_log2) + (r & (p.g - 1));
     *reinterpret_cast<uint2 *>(p.out + orow * 128 + 4 * lane) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     if (p.lse != nullptr && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
@@ -1350,21 +1391,21 @@ tria_status tree_shape(const tria_model_desc &d, const tria_cache_view *c, int m
 }
 
 size_t tree_ws_bytes(const TreeShape &sh) {
-  return kHeaderBytes + (size_t)2 * sh.grid * sh.rows * (128 + 2) * sizeof(float);
+  return kHeaderBytes + (size_t)2 * sh.grid * sh.rows * (128 + 2) * sizeof(float) + (size_t)sh.grid * sizeof(Shared);
 }
 
 template <bool DUALK, int LAYOUT>
 cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t st) {
   const cudaError_t e = launch_attend<DUALK, LAYOUT>(p, sh.grid, st);
   if (e != cudaSuccess || sh.grid == 1) return e;
-  // about two blocks per SM over all units, as far as there are rows for their warps
-  const int64_t units = (int64_t)p.n_seq * p.hkv * sh.tiles;
   const int64_t rows = (int64_t)p.max_draft * p.g < sh.rows ? (int64_t)p.max_draft * p.g : sh.rows;
-  int64_t z = (2 * 148 + units - 1) / units;
-  if (z > (rows + kCombineWarps - 1) / kCombineWarps) z = (rows + kCombineWarps - 1) / kCombineWarps;
-  const dim3 grid((unsigned)(p.n_seq * p.hkv), (unsigned)sh.tiles, (unsigned)z);
-  // launched while attend_kernel still runs: what it reads of the call's inputs
-  // it reads then, and it waits for the partials
+  // one warp per row as far as the blocks (three to an SM) are resident at once
+  const int64_t all = (int64_t)p.n_seq * p.hkv * sh.tiles;
+  const int64_t units = all < sh.grid ? all : sh.grid;  // no more shared ones than CTAs
+  int64_t y = (rows + kCombineWarps - 1) / kCombineWarps;
+  if (y > 3 * 148 / units) y = 3 * 148 / units > 0 ? 3 * 148 / units : 1;
+  const dim3 grid((unsigned)units, (unsigned)y);
+  // launched while attend_kernel still runs; it waits for the partials
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(32 * kCombineWarps);
@@ -1374,7 +1415,7 @@ cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<DUALK, LAYOUT>, p, sh.grid);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<AtCfg<DUALK>::ROWS>, p, sh.grid);
 }
 
 }  // namespace
@@ -1462,6 +1503,7 @@ tria_status tria_tree_attention(const tria_stats *stats, const tria_cache_view *
   p.mask_words = mask_words;
   p.part_o = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
   p.part_ml = p.part_o + (size_t)2 * sh.grid * sh.rows * 128;
+  p.shared = reinterpret_cast<Shared *>(p.part_ml + (size_t)2 * sh.grid * sh.rows * 2);
   if (!query_map(&p.qmap, q, q_tok, q_head, p.hq, p.g, n_tokens) ||
       !cache_map(&p.kmap, cache->k_layers[layer], p.view) || !cache_map(&p.vmap, cache->v_layers[layer], p.view))
     return TRIA_ERR_UNSUPPORTED;
