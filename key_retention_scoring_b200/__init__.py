@@ -418,28 +418,27 @@ def tria_decode_attention(stats, cache, layer, q, scale, out, workspace, lse=Non
                                        _stream(stream)), "tria_decode_attention")
 
 
-def _on_device(where, *tensors):
-    """The serving operators take plain pointers: every (name, tensor or None,
-    types, dimensions, contiguous) must lie on the current device, in the type
-    and layout that the kernels read.  Returns the device's index."""
+def _refuse(where, *tensors):
+    """Says which of (name, tensor or None, types, shape, contiguous) the serving
+    operators cannot take.  They read plain pointers: every tensor must lie on
+    the current device, in the type, shape and layout that the kernels read (a
+    shape entry None is any length)."""
     import torch
 
-    dev = None
-    for name, t, dtypes, dim, contiguous in tensors:
+    for name, t, dtypes, shape, contiguous in tensors:
         if t is None:
             continue
-        d = t.get_device()
-        if dev is None:
-            dev = d
-        if d < 0 or d != dev:
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
             raise TriaError(1, f"{where}: {name} must be on the current CUDA device")
-        if t.dtype not in dtypes or t.dim() != dim:
-            raise TriaError(1, f"{where}: {name} must have {dim} dimensions and type {dtypes[0]}")
+        if t.dtype not in dtypes:
+            raise TriaError(1, f"{where}: {name} must have type {dtypes[0]}")
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            raise TriaError(1, f"{where}: {name} must have shape {shape}, not {tuple(t.shape)}")
         if contiguous and not t.is_contiguous():
             raise TriaError(1, f"{where}: {name} must be contiguous")
-    if dev != torch.cuda.current_device():
-        raise TriaError(1, f"{where}: the tensors must be on the current CUDA device")
-    return dev
+        if not contiguous and t.stride(-1) != 1:
+            raise TriaError(1, f"{where}: {name} must have unit stride inside a head")
+    raise TriaError(1, f"{where}: arguments")
 
 
 def _stream_on(stream, dev):
@@ -452,11 +451,11 @@ def _stream_on(stream, dev):
 def _row_strides(t):
     """(token, head) strides of [tokens, heads, 128]; a dimension of one entry
     never advances, so any stride stands for it."""
-    st, sh, sd = t.stride()
-    if sd != 1:
-        raise TriaError(1, "rows must have unit stride inside a head")
-    return (st if t.shape[0] > 1 else max(st, sh * t.shape[1], 128),
-            sh if t.shape[1] > 1 else 128)
+    st, sh, _ = t.stride()
+    n, h, _ = t.shape
+    if n > 1 and h > 1:
+        return st, sh
+    return (st if n > 1 else max(st, sh * h, 128), sh if h > 1 else 128)
 
 
 def tria_prompt_workspace_size(desc: ModelDesc, n_seq: int) -> int:
@@ -474,16 +473,25 @@ def tria_prompt_attention(desc, q, k, v, seq_starts, scale, out, workspace, lse=
     n_q_heads]."""
     import torch
 
-    bf, where = (torch.bfloat16,), "tria_prompt_attention"
-    dev = _on_device(where, ("q", q, bf, 3, False), ("k", k, bf, 3, False), ("v", v, bf, 3, False),
-                     ("seq_starts", seq_starts, (torch.int32,), 1, True), ("out", out, bf, 3, True),
-                     ("lse", lse, (torch.float32,), 2, True),
-                     ("workspace", workspace, (torch.uint8,), 1, True))
-    n, hq, hkv = q.shape[0], desc.n_q_heads, desc.n_kv_heads
-    kv = (n, hkv, 128)
-    if (q.shape != (n, hq, 128) or k.shape != kv or v.shape != kv or out.shape != q.shape
-            or seq_starts.shape[0] < 2 or (lse is not None and lse.shape != (n, hq))):
-        raise TriaError(1, f"{where}: shapes")
+    where, bf, i32 = "tria_prompt_attention", torch.bfloat16, torch.int32
+    n, hq, hkv, dev = q.shape[0], desc.n_q_heads, desc.n_kv_heads, q.get_device()
+    rows, kv = (n, hq, 128), (n, hkv, 128)
+    # one expression on the way of every call; _refuse says what is wrong
+    if not (q.dtype is bf and k.dtype is bf and v.dtype is bf and out.dtype is bf
+            and seq_starts.dtype is i32 and workspace.dtype is torch.uint8
+            and q.shape == rows and k.shape == kv and v.shape == kv and out.shape == rows
+            and seq_starts.dim() == 1 and workspace.dim() == 1 and seq_starts.shape[0] > 1
+            and q.stride(2) == 1 and k.stride(2) == 1 and v.stride(2) == 1
+            and out.is_contiguous() and seq_starts.is_contiguous() and workspace.is_contiguous()
+            and dev >= 0 and dev == k.get_device() == v.get_device() == out.get_device()
+            == seq_starts.get_device() == workspace.get_device() == torch.cuda.current_device()
+            and (lse is None or (lse.dtype is torch.float32 and lse.shape == (n, hq)
+                                 and lse.is_contiguous() and lse.get_device() == dev))):
+        _refuse(where, ("q", q, (bf,), rows, False), ("k", k, (bf,), kv, False),
+                ("v", v, (bf,), kv, False), ("out", out, (bf,), rows, True),
+                ("seq_starts", seq_starts, (i32,), (None,), True),
+                ("lse", lse, (torch.float32,), (n, hq), True),
+                ("workspace", workspace, (torch.uint8,), (None,), True))
     _check(lib().tria_prompt_attention(
         ctypes.byref(desc), q.data_ptr(), *_row_strides(q), k.data_ptr(), *_row_strides(k),
         v.data_ptr(), *_row_strides(v), n, seq_starts.data_ptr(), seq_starts.shape[0] - 1,
@@ -507,16 +515,25 @@ def tria_tree_attention(stats, cache, layer, q, draft_starts, max_draft, scale, 
     lse optional fp32 [tokens, n_q_heads]."""
     import torch
 
-    bf, where = (torch.bfloat16,), "tria_tree_attention"
-    words = (torch.int32, torch.uint32)
-    dev = _on_device(where, ("q", q, bf, 3, False),
-                     ("draft_starts", draft_starts, (torch.int32,), 1, True), ("out", out, bf, 3, True),
-                     ("mask", mask, words, 2, True), ("lse", lse, (torch.float32,), 2, True),
-                     ("workspace", workspace, (torch.uint8,), 1, True))
-    n, hq = q.shape[0], stats.desc.n_q_heads
-    if (q.shape != (n, hq, 128) or out.shape != q.shape or draft_starts.shape[0] != cache.view.n_seq + 1
-            or (mask is not None and mask.shape[0] != n) or (lse is not None and lse.shape != (n, hq))):
-        raise TriaError(1, f"{where}: shapes")
+    where, bf, i32 = "tria_tree_attention", torch.bfloat16, torch.int32
+    n, hq, dev = q.shape[0], stats.desc.n_q_heads, q.get_device()
+    rows, starts = (n, hq, 128), (cache.view.n_seq + 1,)
+    words = (i32, torch.uint32)
+    if not (q.dtype is bf and out.dtype is bf and draft_starts.dtype is i32
+            and workspace.dtype is torch.uint8 and q.shape == rows and out.shape == rows
+            and draft_starts.shape == starts and workspace.dim() == 1 and q.stride(2) == 1
+            and out.is_contiguous() and draft_starts.is_contiguous() and workspace.is_contiguous()
+            and dev >= 0 and dev == out.get_device() == draft_starts.get_device()
+            == workspace.get_device() == torch.cuda.current_device()
+            and (mask is None or (mask.dtype in words and mask.dim() == 2 and mask.shape[0] == n
+                                  and mask.is_contiguous() and mask.get_device() == dev))
+            and (lse is None or (lse.dtype is torch.float32 and lse.shape == (n, hq)
+                                 and lse.is_contiguous() and lse.get_device() == dev))):
+        _refuse(where, ("q", q, (bf,), rows, False), ("out", out, (bf,), rows, True),
+                ("draft_starts", draft_starts, (i32,), starts, True),
+                ("mask", mask, words, (n, None), True),
+                ("lse", lse, (torch.float32,), (n, hq), True),
+                ("workspace", workspace, (torch.uint8,), (None,), True))
     _check(lib().tria_tree_attention(
         stats.handle, ctypes.byref(cache.view), layer, q.data_ptr(), *_row_strides(q), n,
         draft_starts.data_ptr(), max_draft, _ptr(mask), 0 if mask is None else mask.shape[1], scale,
@@ -537,13 +554,15 @@ def tria_tree_commit(stats, cache, accepted, n_accepted, layer0, layer1, workspa
     of layers [layer0, layer1) and grow the lengths."""
     import torch
 
-    i32, where = (torch.int32,), "tria_tree_commit"
-    dev = _on_device(where, ("accepted", accepted, i32, 2, True),
-                     ("n_accepted", n_accepted, i32, 1, True),
-                     ("workspace", workspace, (torch.uint8,), 1, True))
-    n = cache.view.n_seq
-    if accepted.shape[0] != n or n_accepted.shape[0] != n:
-        raise TriaError(1, f"{where}: shapes")
+    where, i32, n, dev = "tria_tree_commit", torch.int32, cache.view.n_seq, workspace.get_device()
+    if not (accepted.dtype is i32 and n_accepted.dtype is i32 and workspace.dtype is torch.uint8
+            and accepted.dim() == 2 and accepted.shape[0] == n and n_accepted.shape == (n,)
+            and workspace.dim() == 1 and accepted.is_contiguous() and n_accepted.is_contiguous()
+            and workspace.is_contiguous() and dev >= 0
+            and dev == accepted.get_device() == n_accepted.get_device() == torch.cuda.current_device()):
+        _refuse(where, ("accepted", accepted, (i32,), (n, None), True),
+                ("n_accepted", n_accepted, (i32,), (n,), True),
+                ("workspace", workspace, (torch.uint8,), (None,), True))
     _check(lib().tria_tree_commit(stats.handle, ctypes.byref(cache.view), accepted.data_ptr(),
                                   n_accepted.data_ptr(), accepted.shape[1], layer0, layer1,
                                   workspace.data_ptr(), workspace.numel(), _stream_on(stream, dev)),
@@ -563,8 +582,10 @@ def tria_fork_sequences(stats, cache, src, dst, layer0, layer1, workspace, strea
     rows of the block table name are shared."""
     import torch
 
-    where = "tria_fork_sequences"
-    dev = _on_device(where, ("workspace", workspace, (torch.uint8,), 1, True))
+    where, dev = "tria_fork_sequences", workspace.get_device()
+    if not (workspace.dtype is torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous()
+            and dev >= 0 and dev == torch.cuda.current_device()):
+        _refuse(where, ("workspace", workspace, (torch.uint8,), (None,), True))
     if len(src) != len(dst):
         raise TriaError(1, f"{where}: src and dst must have the same length")
     a, b = (np.ascontiguousarray(x, dtype=np.int32) for x in (src, dst))
