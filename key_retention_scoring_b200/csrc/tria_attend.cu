@@ -132,7 +132,7 @@ struct AttendParams {
   float qscale;                                // scale log2(e): base-2 logits
   uint16_t *out;
   float *lse;
-  float *part_o, *part_ml;                     // [2 grid][rows][128], [2 grid][rows][2]
+  float *part_o, *part_ml;                     // partials (part_at), and their m and l [2 grid][rows][2]
   Shared *shared;                              // [grid]
   int32_t *status;
 };
@@ -896,6 +896,27 @@ __device__ __noinline__ bool rescale(uint32_t o_col, float a, uint64_t *done, ui
   return true;
 }
 
+// Four dims (d4) of a row of a partial, in float4: the rows lie side by side, so
+// that warps whose lanes are rows write and read whole lines (row by row, the
+// writes alone took 3 us of a 32K-token call).
+template <int ROWS>
+__device__ __forceinline__ int64_t part_at(int slot, int row, int d4) {
+  return ((int64_t)slot * 32 + d4) * ROWS + row;
+}
+
+// One step of transposing 4 x 4 pieces of 4 words over 4 lanes: lanes MASK apart
+// swap the pieces that lie WORDS apart.
+template <int MASK, int WORDS>
+__device__ __forceinline__ void exchange4(uint32_t (&w)[16], int lane) {
+  const bool upper = (lane & MASK) != 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    if (e & WORDS) continue;
+    const uint32_t got = __shfl_xor_sync(kFull, upper ? w[e] : w[e + WORDS], MASK);
+    if (upper) w[e] = got; else w[e + WORDS] = got;
+  }
+}
+
 template <bool DUALK, int LAYOUT>
 __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem, int warp, int lane,
                           const WaitCtl wc) {
@@ -1098,17 +1119,26 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = y[e];
         }
-        if (mine_row) {
-          if (x.slot >= 0) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o + ((int64_t)x.slot * Cfg::ROWS + row) * 128 + d0);
+        if (x.slot >= 0) {
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o) + part_at<Cfg::ROWS>(x.slot, row, d0 / 4);
+          if (mine_row)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * 128 + d0);
+            for (int e = 0; e < 8; ++e)
+              dst[e * Cfg::ROWS] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          // Four lanes exchange 16-byte pieces so that they write 64 bytes of one
+          // row at a time (each lane its own row: four times the line accesses).
+          uint32_t pw[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                  pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+          for (int e = 0; e < 16; ++e) pw[e] = pack_bf16(o[2 * e], o[2 * e + 1]);
+          exchange4<1, 4>(pw, lane);
+          exchange4<2, 8>(pw, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int64_t to = __shfl_sync(kFull, mine_row ? orow : -1, (lane & ~3) + i);
+            if (to >= 0)
+              *reinterpret_cast<uint4 *>(p.out + to * 128 + d0 + 8 * (lane & 3)) =
+                  make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]);
           }
         }
       }
@@ -1199,14 +1229,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
 
 // ---------------------------------------------------------------------------
 // Partials of a unit that several CTAs worked on, put together: out = sum_c
-// 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.  One warp per row, a lane holds 4
-// dims.  Latency bounds it: the unit's record, then its partials all at once.
+// 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.  A lane has one row and four dims,
+// as the partials lie.  Latency bounds it: the unit's record, then its partials.
 // ---------------------------------------------------------------------------
 constexpr int kCombineWarps = 8;
-constexpr int kBatch = 10;  // partials in flight per row
+constexpr int kBatch = 6;  // partials in flight
 
 template <int ROWS>
-__global__ void __launch_bounds__(32 * kCombineWarps, 3) combine_kernel(const __grid_constant__ AttendParams p, int grid) {
+__global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __grid_constant__ AttendParams p, int grid) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // started beside the end of attend_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the blockIdx.x-th of the CTAs in which a shared unit begins
@@ -1228,49 +1258,52 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 3) combine_kernel(const __
   }
   if (cta < 0) return;
   const Shared u = p.shared[cta];
-  for (int r = blockIdx.y * kCombineWarps + warp; r < u.rows; r += gridDim.y * kCombineWarps) {
+  const int tasks = 32 * ((u.rows + 31) / 32);
+  for (int w = blockIdx.y * kCombineWarps + warp; w < tasks; w += gridDim.y * kCombineWarps) {
+    const int d4 = w & 31, r = (w >> 5) * 32 + lane;
+    if (r >= u.rows) continue;
     // partial c: 0 is the first CTA's
-    auto at = [&](int c) { return (int64_t)(c == 0 ? u.first : u.next + (c - 1) * u.step) * ROWS + r; };
+    auto slot = [&](int c) { return c == 0 ? u.first : u.next + (c - 1) * u.step; };
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b = 0; b <= u.count; b += kBatch) {
-      // the batch's partials and their m and l are on their way at the same time
       const int n = min(kBatch, u.count + 1 - b);
       float4 o[kBatch];
+      float2 ml[kBatch];
 #pragma unroll
-      for (int c = 0; c < kBatch; ++c)
-        if (c < n) o[c] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at(b + c) * 128) + lane);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + at(b + lane) * 2));
-      float top = fmaxf(M, ml.x);
+      for (int c = 0; c < kBatch; ++c) {
+        ml[c] = make_float2(-INFINITY, 0.f);
+        o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < n) {
+          o[c] = __ldcg(reinterpret_cast<const float4 *>(p.part_o) + part_at<ROWS>(slot(b + c), r, d4));
+          ml[c] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + (int64_t)slot(b + c) * ROWS + r);
+        }
+      }
+      float top = M;
 #pragma unroll
-      for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, x));
-      const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - top), back = M == -INFINITY ? 0.f : ex2(M - top);
+      for (int c = 0; c < kBatch; ++c) top = fmaxf(top, ml[c].x);
+      const float back = M == -INFINITY ? 0.f : ex2(M - top);
       M = top;
-      float l = a * ml.y;
-#pragma unroll
-      for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
-      L = fmaf(L, back, l);
+      L *= back;
       acc.x *= back;
       acc.y *= back;
       acc.z *= back;
       acc.w *= back;
 #pragma unroll
       for (int c = 0; c < kBatch; ++c) {
-        const float f = __shfl_sync(kFull, a, c);
-        if (c < n) {
-          acc.x = fmaf(f, o[c].x, acc.x);
-          acc.y = fmaf(f, o[c].y, acc.y);
-          acc.z = fmaf(f, o[c].z, acc.z);
-          acc.w = fmaf(f, o[c].w, acc.w);
-        }
+        const float f = ml[c].x == -INFINITY ? 0.f : ex2(ml[c].x - M);
+        L = fmaf(f, ml[c].y, L);
+        acc.x = fmaf(f, o[c].x, acc.x);
+        acc.y = fmaf(f, o[c].y, acc.y);
+        acc.z = fmaf(f, o[c].z, acc.z);
+        acc.w = fmaf(f, o[c].w, acc.w);
       }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const int64_t orow = (u.row0 + (r >> p.g_log2)) * p.hq + ((int64_t)u.h << p.g_log2) + (r & (p.g - 1));
-    *reinterpret_cast<uint2 *>(p.out + orow * 128 + 4 * lane) =
+    *reinterpret_cast<uint2 *>(p.out + orow * 128 + 4 * d4) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (p.lse != nullptr && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (p.lse != nullptr && d4 == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
 }
 
@@ -1399,11 +1432,11 @@ cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t
   const cudaError_t e = launch_attend<DUALK, LAYOUT>(p, sh.grid, st);
   if (e != cudaSuccess || sh.grid == 1) return e;
   const int64_t rows = (int64_t)p.max_draft * p.g < sh.rows ? (int64_t)p.max_draft * p.g : sh.rows;
-  // one warp per row as far as the blocks (three to an SM) are resident at once
+  // a warp for 32 rows and 4 dims, as far as the blocks (four to an SM) are resident at once
   const int64_t all = (int64_t)p.n_seq * p.hkv * sh.tiles;
   const int64_t units = all < sh.grid ? all : sh.grid;  // no more shared ones than CTAs
-  int64_t y = (rows + kCombineWarps - 1) / kCombineWarps;
-  if (y > 3 * 148 / units) y = 3 * 148 / units > 0 ? 3 * 148 / units : 1;
+  int64_t y = 32 * ((rows + 31) / 32) / kCombineWarps;
+  if (y > 4 * 148 / units) y = 4 * 148 / units > 0 ? 4 * 148 / units : 1;
   const dim3 grid((unsigned)units, (unsigned)y);
   // launched while attend_kernel still runs; it waits for the partials
   cudaLaunchConfig_t cfg{};
