@@ -567,6 +567,7 @@ tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q,
  * (its rows are left as they are).  Paged block ids outside [0, num_blocks)
  * read as zero rows.  The cache is only read.  query_pos is not used.
  * T_s = 1 is a decode step whose own row counts as drafted.
+ * out may not overlap q, mask or the cache.
  * Workspace: tria_tree_workspace_size bytes (256-byte aligned); status flags
  * as in tria_prompt_attention.  Calls that may overlap need separate
  * workspaces.  Equal inputs give equal bits.

@@ -26,15 +26,17 @@
 // A step is 64 keys, and each half has two buffers of S, so the product of the
 // next step is ready while the softmax of this one runs: with one 128-key
 // buffer the chain product, softmax, product set the pace (8448-token prompt,
-// 32 query and 8 KV heads: 597 us against 540).  What bounds it now: the
-// products alone take 449 us of that (Q K^T in steps of 64 keys is bound by
-// shared memory), the exponentials, conversions and maxima alone 433 us.
+// 32 query and 8 KV heads: 597 us against 540 when both were built).  It takes
+// 520 us now, 1126 TFLOP/s.  What bounds it: the products alone take 449 us
+// (Q K^T in steps of 64 keys reads more shared memory than the tensor core can
+// hide), the exponentials, conversions and maxima alone 433 us, and the two
+// share the warps' issue slots.
 // P is rounded to bf16: the second product needs 16-bit operands, the output
 // is rounded to bf16 anyway, and l sums the unrounded weights.
 //
 // What no row may see.  Masked logits become -inf, so masked weights are 0;
 // but 0 x inf and 0 x NaN are NaN, and V rows in a masked place may hold
-// anything (later tokens, other sequences, unused slots).  In blocks that hold
+// anything (later tokens, other sequences, unused slots).  In steps that hold
 // masked places the softmax warps therefore look V over in shared memory
 // before the product reads it, replace what is not finite by 0 and note it;
 // the epilogue then adds those values to the rows that do see them.
@@ -59,8 +61,8 @@ using namespace tc;
 // Waits of the pipeline: the threads sleep in the barrier unit (polling took
 // shared-memory cycles from the products: 1.25 times the time); the clock and
 // the abort flag are looked at after a sleep that ran out.  The limit counts
-// SM cycles at 2 GHz, which is never short: the clock goes one way, while a
-// reading of the global timer was once seen to step back.
+// SM cycles at 2 GHz, which is never short; with the global timer in its place,
+// calls that ran their usual time were now and then reported as expired.
 __device__ __forceinline__ bool poll_on(uint32_t bar, uint32_t parity, const WaitCtl &w) {
   const long long t0 = clock64();
   for (;;) {
@@ -101,12 +103,13 @@ static_assert(2 * kSoftRegs + kRoleRegs == 3 * kLaunchRegs, "register split");
 constexpr int kPacked = 2;                     // LAYOUT of prompts, next to the cache layouts
 constexpr uint32_t kColS = 0, kColO = 256;     // tensor-memory columns: S (and P) of half t at 128 t, O after them
 constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum of a row (base 2) moves only when a block exceeds it by
-// more than this, so most blocks leave O in tensor memory alone; weights stay
+// The running maximum of a row (base 2) moves only when a step exceeds it by
+// more than this, so most steps leave O in tensor memory alone; weights stay
 // below 2^8, well inside fp32 and bf16.
 constexpr float kSlack = 8.f;
 // Of every 8 pairs of exponentials this many run on the FMA pipe, the rest on the
-// special-function unit.
+// special-function unit (16384-token prompt, 64 query heads: 0, 1, 2, 3 of 8 took
+// 3779, 3719, 3870, 3800 us).
 constexpr int kFmaOf8 = 1;
 
 // A unit (sequence, KV head, tile of rows) whose key blocks several CTAs share,
@@ -324,11 +327,10 @@ struct PromptCursor {
 // Paged caches whose rows lie head by head inside a page: one line for each KV
 // head, cut into grid / hkv pieces, and neighbouring CTAs take the same piece
 // for all heads, so that the pages are read whole at about the same time (64
-// sequences of 2048 rows, 8 KV heads, 16-row pages: MEASURED).
+// sequences of 2048 rows, 8 KV heads, 16-row pages: 147 us in one line, 141 in
+// eight).  Where the CTAs are fewer than the heads, one line serves.
 struct Lines {
   int heads, cuts, step;  // KV heads in a line, pieces of a line, CTAs between two pieces
-  // CTA of piece c of head h's line
-  __host__ __device__ __forceinline__ int cta(int c, int h) const { return c * step + (step > 1 ? h : 0); }
 };
 
 template <int LAYOUT>
@@ -492,7 +494,7 @@ struct TileLoads {
     auto page = [&](int j) {  // this lane's block id of key block j
       const int t = (x.kb0 + j) * kBN + at * bs;
       return LAYOUT == TRIA_LAYOUT_PAGED && j < n && at < kBN / bs && t < x.ctx + x.T
-                 ? __ldg(p.view.block_table + (int64_t)x.s * p.view.max_blocks + t / bs)
+                 ? __ldg(p.view.block_table + (int64_t)x.s * p.view.max_blocks + (t >> p.view.block_log2))
                  : 0;
     };
     int blk = page(0);
@@ -709,7 +711,7 @@ __device__ void mma_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tmem
       pp ^= 1u << b;
       tc_fence_after();
       mma_pv(o_col, s_col + 64u * b, v_at + (uint32_t)(Cfg::stage(t, i) * (kTile >> 4)) + b * kHalfRows, kIdescO, g > 0 ? 1u : 0u);
-      if (kNB > 1) elect_commit(&sm.o_done[t]);
+      elect_commit(&sm.o_done[t]);
       if (b == kNB - 1 || g + 1 == mine) elect_commit(&sm.kv_empty[Cfg::stage(t, i)]);
       if (b == kNB - 1 && g + 2 == mine) elect_commit(&sm.kv_empty[Cfg::stage(t, i + 1)]);
       if (g + 1 == mine) elect_commit(&sm.o_full[t]);
@@ -874,9 +876,10 @@ __device__ __noinline__ void add_not_finite(const AttendParams &p, const Item &x
 
 // O *= a for the rows of this warp.  Seldom: kept out of the softmax loop.
 __device__ __noinline__ bool rescale(uint32_t o_col, float a, uint64_t *done, uint32_t parity, const WaitCtl &wc) {
-  // the product before this step's must have been added to O (with one buffer of
-  // S it has: S of this step was issued behind it)
-  if (kNB > 1 && !warp_poll(done, parity, wc)) return false;
+  // The product before this step's must have been added to O.  The one before
+  // that has (S of this step was issued behind it and its barrier came after),
+  // so the phase waited for is this one or the one after it.
+  if (!warp_poll(done, parity, wc)) return false;
   tc_fence_after();
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -927,7 +930,8 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
   const float qs = p.qscale;
   uint32_t sp = 0;           // phases of s_full, bit b
   uint32_t of = 0;           // phases of o_full, bit i
-  int od[2] = {0, 0}, base = 0;  // products of each half so far; ring loads before the item
+  int od[2] = {0, 0};        // products of each half before the item
+  int base = 0;              // loads of this half's ring before the item
   for (int it = 0;; ++it) {
     if (!warp_poll(&sm.it_full[it & 1], (uint32_t)((it >> 1) & 1), wc)) return;
     const Item x = sm.item[it & 1];
@@ -1523,6 +1527,7 @@ tria_status tria_tree_attention(const tria_stats *stats, const tria_cache_view *
   if ((st = check_desc(d)) != TRIA_OK) return st;
   if ((st = check_rows(q, q_tok, q_head, n_tokens, starts, scale, out, lse)) != TRIA_OK) return st;
   if (max_draft < 1 || max_draft > cache->max_seq_len) return TRIA_ERR_INVALID_ARG;
+  if (cache->max_seq_len > INT32_MAX - 1024) return TRIA_ERR_UNSUPPORTED;  // key indices of a block past the end
   if (mask != nullptr && (!aligned(mask, 4) || mask_words < (max_draft + 31) / 32)) return TRIA_ERR_INVALID_ARG;
   TreeShape sh;
   if ((st = tree_shape(d, cache, max_draft, &sh)) != TRIA_OK) return st;

@@ -216,7 +216,7 @@ __host__ __device__ __forceinline__ bool compresses(const Geom &g, int n, int lr
 // ---------------------------------------------------------------------------
 // A checked cache view for kernels that address rows themselves.
 struct RowsView {
-  int layout, block_size, max_blocks;
+  int layout, block_size, block_log2, max_blocks;
   int n_seq, n_layers, hkv, max_seq_len;
   int64_t s_seq, s_head, s_tok, s_blk, num_blocks;
   const int32_t *block_table;
@@ -251,8 +251,8 @@ __host__ __device__ __forceinline__ bool view_row(const RowsView &v, int s, int 
     *off = (int64_t)s * v.s_seq + (int64_t)h * v.s_head + (int64_t)t * v.s_tok;
     return true;
   }
-  const int blk = v.block_table[(int64_t)s * v.max_blocks + t / v.block_size];
-  *off = (int64_t)blk * v.s_blk + (int64_t)(t % v.block_size) * v.s_tok + (int64_t)h * v.s_head;
+  const int blk = v.block_table[(int64_t)s * v.max_blocks + (t >> v.block_log2)];
+  *off = (int64_t)blk * v.s_blk + (int64_t)(t & (v.block_size - 1)) * v.s_tok + (int64_t)h * v.s_head;
   return blk >= 0 && blk < v.num_blocks;
 }
 

@@ -41,6 +41,7 @@ tria_status make_rows_view(const tria_stats *stats, const tria_cache_view *c, in
   RowsView v{};
   v.layout = c->layout;
   v.block_size = paged ? c->block_size : 1;
+  while ((1 << v.block_log2) < v.block_size) ++v.block_log2;  // a power of two
   v.max_blocks = paged ? c->max_blocks_per_seq : 0;
   v.n_seq = c->n_seq;
   v.n_layers = desc->n_layers;
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
   const int nt = min(kForkRows, N - t0);
   uint16_t *base = is_v ? p.at.v[l] : p.at.k[l];
   const bool paged = v.layout == TRIA_LAYOUT_PAGED;
-  const int bs = v.block_size, bs_log2 = __ffs(bs) - 1;  // a power of two
-  const int b0 = paged ? t0 / bs : 0, nb = paged ? (t0 + nt - 1) / bs - b0 + 1 : 1;
+  const int bs = v.block_size, bs_log2 = v.block_log2;
+  const int b0 = paged ? t0 >> bs_log2 : 0, nb = paged ? ((t0 + nt - 1) >> bs_log2) - b0 + 1 : 1;
   __shared__ int64_t s_from[kForkBlocks], s_to[kForkDst][kForkBlocks];
   __shared__ uint32_t s_need[kForkBlocks];
   for (int d = d0; d < d1; d += kForkDst) {
