@@ -89,8 +89,8 @@ struct LayerPtrs {
 // first chunk's rows are on their way (a source out of range is not read), and
 // one barrier serves both.
 // ---------------------------------------------------------------------------
-constexpr int kMoveU = 4;
-constexpr int kMoveRows = kMoveU * kMoveThreads / kPieces;  // rows of a chunk: 64
+constexpr int kMoveU = 2;
+constexpr int kMoveRows = kMoveU * kMoveThreads / kPieces;  // rows of a chunk: 32
 constexpr int kRowStep = kMoveThreads / kPieces;            // rows of one pass of the block: 16
 
 struct CommitParams {
@@ -104,7 +104,7 @@ struct CommitParams {
   int32_t *status;
 };
 
-__global__ void __launch_bounds__(kMoveThreads, 4) commit_kernel(const __grid_constant__ CommitParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 6) commit_kernel(const __grid_constant__ CommitParams p) {
   const RowsView &v = p.view;
   const int s = blockIdx.x / p.nl, l = blockIdx.x % p.nl;
   const int tid = threadIdx.x, layer = p.layer0 + l, hkv = v.hkv;
