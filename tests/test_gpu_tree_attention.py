@@ -307,3 +307,52 @@ def test_equal_bits_on_another_stream_and_from_graphs():
         assert T.tria_read_device_status(d.ws) == 0
     finally:
         st.free()
+
+
+def test_offsets_past_32_bits():
+    # 16 sequences x 8 heads x 131300 rows x 128: the last rows lie past 2^31 elements
+    lens = [0] * 15 + [131200]
+    st = Store(T, 1, 16, 8, lens, 131300, seed=16)
+    try:
+        assert st.k.numel() > 2 ** 31
+        d = Drafts(st, 16, [0] * 15 + [7], seed=16)
+        d.run()
+        d.check(heads=[0, 15])
+        # the accepted rows of the last sequence, and a copy of it in the first
+        want = [st.rows(x, 0, 15, 7, 131207)[131200 + torch.tensor([1, 4, 6], device="cuda")] for x in (st.k, st.v)]
+        acc = torch.tensor([[0, 0, 0]] * 15 + [[1, 4, 6]], dtype=torch.int32, device="cuda")
+        cnt = torch.tensor([0] * 15 + [3], dtype=torch.int32, device="cuda")
+        ws = T.alloc_workspace(T.tria_commit_workspace_size(st.stats, st.cache))
+        T.tria_tree_commit(st.stats, st.cache, acc, cnt, 0, 1, ws)
+        wf = T.alloc_workspace(T.tria_fork_workspace_size(st.stats, st.cache))
+        T.tria_fork_sequences(st.stats, st.cache, [15], [14], 0, 1, wf)
+        for x, w in zip((st.k, st.v), want):
+            assert torch.equal(st.rows(x, 0, 15, 7, 131203)[-3:], w)
+            assert torch.equal(x[0, 14, :, :131203], x[0, 15, :, :131203])
+        assert st.lens.tolist()[13:] == [0, 131203, 131203]
+    finally:
+        st.free()
+
+
+def test_two_calls_at_once():
+    st = Store(T, 1, 32, 8, [5000, 700], 5100, seed=17)
+    try:
+        d = Drafts(st, 32, [20, 3], seed=17)
+        e = Drafts(st, 32, [3, 60], seed=18, mask=False)
+        d.run()
+        e.run()
+        torch.cuda.synchronize()
+        a, b = d.out.clone(), e.out.clone()
+        d.out.fill_(1.0)
+        e.out.fill_(1.0)
+        one, two = torch.cuda.Stream(), torch.cuda.Stream()
+        for s in (one, two):
+            s.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            d.run(stream=one)
+            e.run(stream=two)
+        torch.cuda.synchronize()
+        assert torch.equal(a, d.out) and torch.equal(b, e.out)
+        assert T.tria_read_device_status(d.ws) == 0 and T.tria_read_device_status(e.ws) == 0
+    finally:
+        st.free()
