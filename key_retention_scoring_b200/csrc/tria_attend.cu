@@ -549,6 +549,9 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
   const uint64_t qpol = normal_policy();
   TileLoads<DUALK, LAYOUT, false> keys;
   Cursor cur;
+  // The block may have started before the kernel before it in the stream ended.
+  // Nothing is read or written before this; the other roles begin with an item.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   cur.init(p, lane);
   int it = 0, q_loads = 0;
   bool ok = true;
@@ -1386,6 +1389,23 @@ cudaError_t sm_count(int *sms) {
   return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
+// A launch whose blocks may start while the kernel before it in the stream ends;
+// the kernels wait for that one (griddepcontrol.wait) before they touch memory.
+template <class Kernel, class... Args>
+cudaError_t launch_early(Kernel kernel, dim3 grid, int threads, int smem, cudaStream_t st, const Args &...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <bool DUALK, int LAYOUT>
 cudaError_t launch_attend(const AttendParams &p, int grid, cudaStream_t st) {
   const int smem = (int)sizeof(AtSmem<DUALK>);
@@ -1404,8 +1424,7 @@ cudaError_t launch_attend(const AttendParams &p, int grid, cudaStream_t st) {
     if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
     attr_dev = dev;
   }
-  attend_kernel<DUALK, LAYOUT><<<grid, kAtThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(attend_kernel<DUALK, LAYOUT>, dim3((unsigned)grid), kAtThreads, smem, st, p);
 }
 
 // Tiles of rows per (sequence, KV head) at most, and rows of a partial.
@@ -1444,17 +1463,7 @@ cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t
   int64_t y = 32 * ((rows + 31) / 32) / kCombineWarps;
   if (y > 4 * 148 / units) y = 4 * 148 / units > 0 ? 4 * 148 / units : 1;
   const dim3 grid((unsigned)units, (unsigned)y);
-  // launched while attend_kernel still runs; it waits for the partials
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(32 * kCombineWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<AtCfg<DUALK>::ROWS>, p, sh.grid);
+  return launch_early(combine_kernel<AtCfg<DUALK>::ROWS>, grid, 32 * kCombineWarps, 0, st, p, sh.grid);
 }
 
 }  // namespace
