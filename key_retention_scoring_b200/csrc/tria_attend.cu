@@ -549,9 +549,6 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
   const uint64_t qpol = normal_policy();
   TileLoads<DUALK, LAYOUT, false> keys;
   Cursor cur;
-  // The block may have started before the kernel before it in the stream ended.
-  // Nothing is read or written before this; the other roles begin with an item.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   cur.init(p, lane);
   int it = 0, q_loads = 0;
   bool ok = true;
@@ -1174,6 +1171,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the block's memory is full, with no room to move the tiles to a boundary
   if (smem_u32(smem_dyn) & 1023u) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) atomicOr(p.status, 2);
     return;
   }
@@ -1209,6 +1207,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  // The block may have started beside the kernel before it in the stream: no global
+  // memory is touched before this, and no role's limit on its waits runs before it
+  // (that kernel may take longer than the limit).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const WaitCtl wc = wait_ctl(&sm.abort_flag, p.status, 0);
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));

@@ -214,3 +214,47 @@ def test_no_tokens_is_no_work():
     p = Prompt(8, 2, [0, 0], seed=14)
     p.run()
     assert T.tria_read_device_status(p.ws) == 0
+
+
+def test_calls_that_read_one_another_between_copies_and_joined_streams():
+    # A call's blocks may be resident before the kernel, copy or fill before it has ended.
+    lens = [700, 3, 1500]
+    p, q = Prompt(8, 8, lens, seed=15), Prompt(8, 8, lens, seed=16)
+    keep_q, side = q.q.clone(), torch.cuda.Stream()
+    mid = torch.empty_like(p.out)
+
+    def chain(wait):
+        main = torch.cuda.current_stream()
+        q.q.copy_(keep_q)                       # a copy, then a call that reads it
+        q.run()
+        wait()
+        p.out.zero_()                           # a fill, then a call over it
+        T.tria_prompt_attention(p.desc, q.out, p.k, p.v, p.starts, SCALE, p.out, p.ws, lse=p.lse)
+        wait()
+        T.tria_prompt_attention(p.desc, p.out, q.out, p.out, p.starts, SCALE, mid, p.ws, lse=p.lse)
+        wait()
+        side.wait_stream(main)                  # two streams, and their join
+        with torch.cuda.stream(side):
+            T.tria_prompt_attention(p.desc, mid, p.k, p.v, p.starts, SCALE, p.out, p.ws, lse=p.lse)
+        T.tria_prompt_attention(q.desc, mid, mid, q.v, q.starts, SCALE, q.out, q.ws, lse=q.lse)
+        main.wait_stream(side)
+        wait()
+        T.tria_prompt_attention(p.desc, q.out, p.out, q.out, p.starts, SCALE, mid, p.ws, lse=p.lse)
+        q.q.copy_(mid)                          # a copy that reads the last call's rows
+
+    chain(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    want = q.q.clone()
+    for _ in range(5):
+        chain(lambda: None)
+        torch.cuda.synchronize()
+        assert torch.equal(want, q.q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(lambda: None)
+    for _ in range(5):
+        q.q.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want, q.q)
+    assert T.tria_read_device_status(p.ws) == 0 and T.tria_read_device_status(q.ws) == 0
