@@ -448,11 +448,10 @@ def _stream_on(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _row_strides(t):
-    """(token, head) strides of [tokens, heads, 128]; a dimension of one entry
-    never advances, so any stride stands for it."""
-    st, sh, _ = t.stride()
-    n, h, _ = t.shape
+def _row_strides(strides, n, h):
+    """(token, head) strides of [n tokens, h heads, 128]; a dimension of one
+    entry never advances, so any stride stands for it."""
+    st, sh, _ = strides
     if n > 1 and h > 1:
         return st, sh
     return (st if n > 1 else max(st, sh * h, 128), sh if h > 1 else 128)
@@ -479,12 +478,12 @@ def tria_prompt_attention(desc, q, k, v, seq_starts, scale, out, workspace, lse=
     # one expression on the way of every call; _refuse says what is wrong
     if not (q.dtype is bf and k.dtype is bf and v.dtype is bf and out.dtype is bf
             and seq_starts.dtype is i32 and workspace.dtype is torch.uint8
-            and q.shape == rows and k.shape == kv and v.shape == kv and out.shape == rows
-            and seq_starts.dim() == 1 and workspace.dim() == 1 and seq_starts.shape[0] > 1
-            and q.stride(2) == 1 and k.stride(2) == 1 and v.stride(2) == 1
+            and q.shape == out.shape == rows and k.shape == v.shape == kv
+            and seq_starts.dim() == workspace.dim() == 1 and seq_starts.shape[0] > 1
+            and (sq := q.stride())[2] == (sk := k.stride())[2] == (sv := v.stride())[2] == 1
             and out.is_contiguous() and seq_starts.is_contiguous() and workspace.is_contiguous()
             and dev >= 0 and dev == k.get_device() == v.get_device() == out.get_device()
-            == seq_starts.get_device() == workspace.get_device() == torch.cuda.current_device()
+            == seq_starts.get_device() == workspace.get_device() == torch._C._cuda_getDevice()
             and (lse is None or (lse.dtype is torch.float32 and lse.shape == (n, hq)
                                  and lse.is_contiguous() and lse.get_device() == dev))):
         _refuse(where, ("q", q, (bf,), rows, False), ("k", k, (bf,), kv, False),
@@ -493,8 +492,8 @@ def tria_prompt_attention(desc, q, k, v, seq_starts, scale, out, workspace, lse=
                 ("lse", lse, (torch.float32,), (n, hq), True),
                 ("workspace", workspace, (torch.uint8,), (None,), True))
     _check(lib().tria_prompt_attention(
-        ctypes.byref(desc), q.data_ptr(), *_row_strides(q), k.data_ptr(), *_row_strides(k),
-        v.data_ptr(), *_row_strides(v), n, seq_starts.data_ptr(), seq_starts.shape[0] - 1,
+        ctypes.byref(desc), q.data_ptr(), *_row_strides(sq, n, hq), k.data_ptr(), *_row_strides(sk, n, hkv),
+        v.data_ptr(), *_row_strides(sv, n, hkv), n, seq_starts.data_ptr(), seq_starts.shape[0] - 1,
         scale, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
         _stream_on(stream, dev)), where)
 
@@ -521,10 +520,10 @@ def tria_tree_attention(stats, cache, layer, q, draft_starts, max_draft, scale, 
     words = (i32, torch.uint32)
     if not (q.dtype is bf and out.dtype is bf and draft_starts.dtype is i32
             and workspace.dtype is torch.uint8 and q.shape == rows and out.shape == rows
-            and draft_starts.shape == starts and workspace.dim() == 1 and q.stride(2) == 1
+            and draft_starts.shape == starts and workspace.dim() == 1 and (sq := q.stride())[2] == 1
             and out.is_contiguous() and draft_starts.is_contiguous() and workspace.is_contiguous()
             and dev >= 0 and dev == out.get_device() == draft_starts.get_device()
-            == workspace.get_device() == torch.cuda.current_device()
+            == workspace.get_device() == torch._C._cuda_getDevice()
             and (mask is None or (mask.dtype in words and mask.dim() == 2 and mask.shape[0] == n
                                   and mask.is_contiguous() and mask.get_device() == dev))
             and (lse is None or (lse.dtype is torch.float32 and lse.shape == (n, hq)
@@ -535,7 +534,7 @@ def tria_tree_attention(stats, cache, layer, q, draft_starts, max_draft, scale, 
                 ("lse", lse, (torch.float32,), (n, hq), True),
                 ("workspace", workspace, (torch.uint8,), (None,), True))
     _check(lib().tria_tree_attention(
-        stats.handle, ctypes.byref(cache.view), layer, q.data_ptr(), *_row_strides(q), n,
+        stats.handle, ctypes.byref(cache.view), layer, q.data_ptr(), *_row_strides(sq, n, hq), n,
         draft_starts.data_ptr(), max_draft, _ptr(mask), 0 if mask is None else mask.shape[1], scale,
         out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(), _stream_on(stream, dev)),
         where)
