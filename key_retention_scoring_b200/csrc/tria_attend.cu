@@ -169,7 +169,7 @@ struct AtSmem {
   uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_done[2], o_full[2], it_full[2], it_empty[2], ml_full, o_read, drain[2];
   Item item[2];
   float ml[DUALK ? 2 : 1][2][DUALK ? 128 : 1];
-  volatile int poison[2];
+  volatile int poison[4];  // by item: one half may be two items ahead of the other
   uint32_t tmem_base;
   volatile int abort_flag;
 };
@@ -951,7 +951,9 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
       if constexpr (MASKED) {
         const int i = base + 2 * (g / kNB) + 1;
         if (!warp_poll(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc)) return false;
-        if (clean_v(sm.kv[Cfg::stage(t, i)] + b * (kHN * 128), r, &sm.poison[it & 1], it + 1))
+        const bool found = clean_v(sm.kv[Cfg::stage(t, i)] + b * (kHN * 128), r, &sm.poison[it & 3], it + 1);
+        // DUALQ: what this thread found clean the other half's may have replaced
+        if (found || !DUALK)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       if (!warp_poll(&sm.s_full[t][b], (sp >> b) & 1u, wc)) return false;
@@ -1088,7 +1090,7 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
     }
     tc_fence_after();
     if (!idle) {
-      const bool poisoned = sm.poison[it & 1] == it + 1;
+      const bool poisoned = sm.poison[it & 3] == it + 1;
       const bool mine_row = tok < x.T;
       const float inv = x.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const int row = (DUALK ? 0 : 128 * t) + r;
@@ -1192,8 +1194,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
       mbar_init(&sm.drain[i], 1);
       mbar_init(&sm.it_full[i], 1);
       mbar_init(&sm.it_empty[i], kSoftWarps + 3);
-      sm.poison[i] = 0;
     }
+    for (int i = 0; i < 4; ++i) sm.poison[i] = 0;
     mbar_init(&sm.ml_full, kSoftWarps);
     mbar_init(&sm.o_read, kSoftWarps);
     sm.abort_flag = 0;

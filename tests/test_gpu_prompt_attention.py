@@ -167,6 +167,25 @@ def test_a_value_that_is_no_number_reaches_the_rows_that_see_it(bad):
         assert bool(torch.isfinite(torch.cat([p.out[:, h, :17], p.out[:, h, 18:]], 1)).all())
 
 
+def test_values_that_are_no_numbers_in_many_short_sequences():
+    # several short items for each processor, one after another in either half
+    lens = [1 + (37 * i) % 190 for i in range(120)]
+    p = Prompt(32, 8, lens, seed=17)
+    want = torch.ones(p.out.shape[:2], dtype=torch.bool, device="cuda")  # dim 17 is finite
+    at = 0
+    for i, n in enumerate(lens):
+        j, h = (11 * i) % n, i % 8
+        p.v[at + j, h, 17] = [float("inf"), float("-inf"), float("nan")][i % 3]
+        want[at + j: at + n, 4 * h: 4 * h + 4] = False
+        at += n
+    for _ in range(20):
+        p.out.fill_(7.0)
+        p.run()
+        fin = torch.isfinite(p.out)
+        assert torch.equal(fin[:, :, 17], want)
+        assert bool(fin[:, :, :17].all()) and bool(fin[:, :, 18:].all())
+
+
 @pytest.mark.parametrize("starts", [[0, 10, 5, 20], [-1, 10, 15, 20], [0, 10, 15, 21]])
 def test_bad_starts_are_flagged(starts):
     p = Prompt(8, 2, [10, 5, 5], seed=11)
