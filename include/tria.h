@@ -439,7 +439,10 @@ tria_status tria_calib_finalize(const tria_model_desc *desc, const double *acc, 
  * [0, max_seq_len] (such a unit is skipped and its kept row is all -1).
  * Bit 1: a wait of the scoring kernel ran out (tria_params.wait_limit_ns);
  * the kernel stopped early and the call's scores, kept rows and compaction
- * are undefined.  Synchronises `stream`.  *flags_out = 0 means none.
+ * are undefined.  In the workspace of a prompt or tree attention call: a wait
+ * of that kernel ran out (tria_set_attention_wait_limit), and what out and lse
+ * hold in the rows of the call's sequences is undefined (other rows are left
+ * as they are).  Synchronises `stream`.  *flags_out = 0 means none.
  * The flags start undefined in a fresh workspace: read (and so clear) them
  * once before the first call.
  */
@@ -492,6 +495,19 @@ tria_status tria_decode_attention(const tria_stats *stats, const tria_cache_view
                                   int layer, const void *q, float scale, float *out,
                                   float *lse, float *logits, void *workspace,
                                   size_t workspace_bytes, tria_stream_t stream);
+
+/*
+ * tria_set_attention_wait_limit - bound, in ns, of every wait of the prompt and
+ * tree attention kernels on their pipeline, for the calls made from this host
+ * thread from now on (a captured call keeps the bound it was captured with);
+ * 0 = 2 s, as before the first call.  It counts processor cycles at 2 GHz and is
+ * looked at when a waiting thread's sleep has run out, so a short wait may end
+ * well under any bound.  A wait that runs out sets status bit 1 (tria_read_device_status); the kernel
+ * lets its own loads and MMAs land and returns.  A limit far below a kernel's
+ * run time makes that happen on purpose (tests of the abort path).
+ * Errors: INVALID_ARG (ns < 0).
+ */
+tria_status tria_set_attention_wait_limit(int64_t ns);
 
 /*
  * tria_prompt_attention - attention over whole prompts: what fills the cache

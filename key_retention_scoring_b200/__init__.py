@@ -35,7 +35,7 @@ EXPORTS = ["tria_status_string", "tria_version", "tria_load_stats", "tria_free_s
            "tria_write_stats_file", "tria_read_stats_file", "tria_prompt_workspace_size",
            "tria_prompt_attention", "tria_tree_workspace_size", "tria_tree_attention",
            "tria_commit_workspace_size", "tria_tree_commit", "tria_fork_workspace_size",
-           "tria_fork_sequences"]
+           "tria_fork_sequences", "tria_set_attention_wait_limit"]
 STATIC_SCRATCH_BYTES = 32 * 1024 * 1024   # TRIA_STATIC_SCRATCH_BYTES
 
 
@@ -124,6 +124,7 @@ def lib() -> ctypes.CDLL:
                                        _VP]
     i64, size = ctypes.c_int64, ctypes.c_size_t
     view = ctypes.POINTER(CacheView)
+    L.tria_set_attention_wait_limit.argtypes = [i64]
     L.tria_prompt_workspace_size.argtypes = [ctypes.POINTER(ModelDesc), _I, ctypes.POINTER(size)]
     L.tria_prompt_attention.argtypes = [ctypes.POINTER(ModelDesc), _VP, i64, i64, _VP, i64, i64, _VP,
                                         i64, i64, i64, _VP, _I, ctypes.c_float, _VP, _VP, _VP, size,
@@ -455,6 +456,12 @@ def _row_strides(strides, n, h):
     if n > 1 and h > 1:
         return st, sh
     return (st if n > 1 else max(st, sh * h, 128), sh if h > 1 else 128)
+
+
+def tria_set_attention_wait_limit(ns: int):
+    """Bound of each wait of the prompt and tree attention kernels, for the calls
+    made from this host thread from now on (0: 2 s)."""
+    _check(lib().tria_set_attention_wait_limit(int(ns)), "tria_set_attention_wait_limit")
 
 
 def tria_prompt_workspace_size(desc: ModelDesc, n_seq: int) -> int:

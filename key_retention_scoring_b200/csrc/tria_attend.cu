@@ -68,7 +68,7 @@ __device__ __forceinline__ bool poll_on(uint32_t bar, uint32_t parity, const Wai
   for (;;) {
     if (mbar_try_sleep(bar, parity, w.hint_ns)) return true;
     if (*w.abort_flag) return false;
-    if (clock64() - t0 > (long long)(2 * w.limit_ns)) {
+    if ((uint64_t)(clock64() - t0) / 2 > w.limit_ns) {
       flag_expiry(w);
       return false;
     }
@@ -138,6 +138,7 @@ struct AttendParams {
   float *part_o, *part_ml;                     // partials (part_at), and their m and l [2 grid][rows][2]
   Shared *shared;                              // [grid]
   int32_t *status;
+  uint64_t wait_ns;                            // bound of every wait (0: 2 s)
 };
 
 // One piece of work: rows of tokens [tok0, ..) of (s, h) against key blocks [kb0, kb1).
@@ -170,6 +171,7 @@ struct AtSmem {
   Item item[2];
   float ml[DUALK ? 2 : 1][2][DUALK ? 128 : 1];
   volatile int poison[4];  // by item: one half may be two items ahead of the other
+  int last_load[2][AtCfg<DUALK>::RINGS], q_loads;  // what the K and the V warp loaded, as they leave
   uint32_t tmem_base;
   volatile int abort_flag;
 };
@@ -533,14 +535,31 @@ struct TileLoads {
     return true;
   }
 
-  // aborted: this warp's loads still in flight must land before the block exits
-  // (of those ST and more back, the stage was used again only after they had)
-  __device__ void drain(AtSmem<DUALK> &sm, const WaitCtl &wc) {
-    for (int t = 0; t < Cfg::RINGS; ++t)
-      for (int i = max(IS_V ? 1 : 0, done[t] - 2 * (Cfg::ST / 2)); i <= done[t]; i += 2)
-        mbar_drain(&sm.kv_full[Cfg::stage(t, i)], Cfg::phase(i), wc.status);
+  // as the warp leaves: what drain_loads may have to wait for
+  __device__ void leave(AtSmem<DUALK> &sm) const {
+    for (int t = 0; t < Cfg::RINGS; ++t) sm.last_load[IS_V ? 1 : 0][t] = done[t];
   }
 };
+
+// After a wait ran out, when every role has left (one thread): loads still in
+// flight must land before the block exits, those of a load warp that had come to
+// the end of its work included.  A stage passes from one load warp to the other,
+// so the last load into it, of either, is the one to wait for: it was issued when
+// those before it had landed.
+template <bool DUALK>
+__device__ void drain_loads(AtSmem<DUALK> &sm, int32_t *status) {
+  using Cfg = AtCfg<DUALK>;
+  for (int t = 0; t < Cfg::RINGS; ++t) {
+    for (int s = 0; s < Cfg::ST; ++s) {
+      int last = -1;  // of the K warp's even loads and the V warp's odd ones
+      for (int w = 0; w < 2; ++w)
+        for (int i = sm.last_load[w][t]; i >= w && i > last; i -= 2)
+          if (i % Cfg::ST == s) last = i;
+      if (last >= 0) mbar_drain(&sm.kv_full[Cfg::stage(t, last)], Cfg::phase(last), status);
+    }
+  }
+  if (sm.q_loads > 0) mbar_drain(&sm.q_full, (uint32_t)((sm.q_loads - 1) & 1), status);
+}
 
 // Items of work for everyone, Q and K.
 template <bool DUALK, int LAYOUT, class Cursor>
@@ -551,7 +570,6 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
   Cursor cur;
   cur.init(p, lane);
   int it = 0, q_loads = 0;
-  bool ok = true;
   Item x{};
   auto wait = [&](uint64_t *bar, int phase) {
     bool good = true;
@@ -561,7 +579,7 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
   for (;;) {
     const bool more = cur.next(p, lane, x);
     const int slot = it & 1;
-    if (it >= 2 && !(ok = wait(&sm.it_empty[slot], (it >> 1) - 1))) break;
+    if (it >= 2 && !wait(&sm.it_empty[slot], (it >> 1) - 1)) break;
     if (lane == 0) {
       if (!more) x.kb1 = -1;
       sm.item[slot] = x;
@@ -572,7 +590,7 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
       if (lane == 0) cur.finish(p);
       break;
     }
-    if (it > 1 && !(ok = wait(&sm.q_empty, it - 2))) break;
+    if (it > 1 && !wait(&sm.q_empty, it - 2)) break;
     if (lane == 0) mbar_arrive_expect_tx(&sm.q_full, Cfg::QT * kTile);
     __syncwarp();
     if (lane < 2 * Cfg::QT) {
@@ -581,11 +599,11 @@ __device__ void load_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, co
                   (int)x.row0 + x.tok0 + t * (kRows >> p.g_log2), 0, &sm.q_full, qpol);
     }
     ++q_loads;
-    if (!(ok = keys.item(p, sm, x, lane, wc))) break;
+    if (!keys.item(p, sm, x, lane, wc)) break;
   }
-  if (!ok && lane == 0) {
-    keys.drain(sm, wc);
-    if (q_loads > 0) mbar_drain(&sm.q_full, (q_loads - 1) & 1, wc.status);
+  if (lane == 0) {
+    keys.leave(sm);
+    sm.q_loads = q_loads;
   }
   __syncwarp();
 }
@@ -602,7 +620,7 @@ __device__ void value_role(const AttendParams &p, AtSmem<DUALK> &sm, int lane, c
     if (x.kb1 < 0) break;
     ok = values.item(p, sm, x, lane, wc);
   }
-  if (!ok && lane == 0) values.drain(sm, wc);
+  if (lane == 0) values.leave(sm);
   __syncwarp();
 }
 
@@ -1213,7 +1231,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   // memory is touched before this, and no role's limit on its waits runs before it
   // (that kernel may take longer than the limit).
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const WaitCtl wc = wait_ctl(&sm.abort_flag, p.status, 0);
+  const WaitCtl wc = wait_ctl(&sm.abort_flag, p.status, p.wait_ns);
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     soft_role<DUALK, LAYOUT>(p, sm, tmem, warp, lane, wc);
@@ -1236,6 +1254,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (tid == 0 && sm.abort_flag) drain_loads<DUALK>(sm, p.status);
 }
 
 // ---------------------------------------------------------------------------
@@ -1322,6 +1341,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
+thread_local int64_t g_wait_ns = 0;  // tria_set_attention_wait_limit
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool strides_ok(int64_t tok, int64_t head) { return tok > 0 && head > 0 && tok % 8 == 0 && head % 8 == 0; }
@@ -1358,6 +1379,7 @@ void fill_rows(AttendParams &p, const tria_model_desc &d, int n_seq, int64_t n_t
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
   p.status = reinterpret_cast<int32_t *>(static_cast<unsigned char *>(ws) + 4);
+  p.wait_ns = (uint64_t)g_wait_ns;
 }
 
 // q as tiles of 128 rows: 128 / G tokens x the G heads of a KV head x 64 dims
@@ -1477,6 +1499,12 @@ cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t
 using namespace tria;
 
 extern "C" {
+
+tria_status tria_set_attention_wait_limit(int64_t ns) {
+  if (ns < 0) return TRIA_ERR_INVALID_ARG;
+  g_wait_ns = ns;
+  return TRIA_OK;
+}
 
 tria_status tria_prompt_workspace_size(const tria_model_desc *desc, int n_seq, size_t *bytes) {
   if (desc == nullptr || bytes == nullptr || n_seq < 1 || n_seq > TRIA_MAX_SEQS) return TRIA_ERR_INVALID_ARG;
