@@ -114,7 +114,9 @@ constexpr int kFmaOf8 = 1;
 
 // A unit (sequence, KV head, tile of rows) whose key blocks several CTAs share,
 // written down by the CTA that has its first block: its rows, the slot of the
-// first partial, and those of the others.
+// first partial, and those of the others.  Every CTA of a call writes one, first
+// of all without rows: a CTA that leaves early must not leave combine_kernel what
+// an earlier call of the workspace wrote there.
 struct Shared {
   int64_t row0;          // first token's row in the output
   int h, rows;           // rows: 0 when no unit begins in this CTA and goes on in the next
@@ -1189,9 +1191,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   AtSmem<DUALK> &sm = *reinterpret_cast<AtSmem<DUALK> *>(smem_dyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // by the thread that writes the CTA's record at the end
+  auto no_record = [&] {
+    if (LAYOUT != kPacked && tid == 32 * kLoadWarp) p.shared[blockIdx.x].rows = 0;
+  };
   // the block's memory is full, with no room to move the tiles to a boundary
   if (smem_u32(smem_dyn) & 1023u) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    no_record();
     if (tid == 0) atomicOr(p.status, 2);
     return;
   }
@@ -1231,6 +1238,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
   // memory is touched before this, and no role's limit on its waits runs before it
   // (that kernel may take longer than the limit).
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  no_record();
   const WaitCtl wc = wait_ctl(&sm.abort_flag, p.status, p.wait_ns);
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));

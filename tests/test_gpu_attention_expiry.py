@@ -21,7 +21,9 @@ if not torch.cuda.is_available():
 
 import key_retention_scoring_b200 as T  # noqa: E402
 from key_retention_scoring_b200 import build as tria_build  # noqa: E402
+from tests.serving_helpers import Store  # noqa: E402
 from tests.test_gpu_prompt_attention import Prompt  # noqa: E402
+from tests.test_gpu_tree_attention import Drafts  # noqa: E402
 
 WAIT_EXPIRED = 2
 
@@ -69,3 +71,33 @@ def test_prompt_wait_expires_and_the_next_call_is_right(lens):
     p.run()
     p.check(seqs=range(0, len(lens), 17), heads=[0, 31])
     assert T.tria_read_device_status(p.ws) == 0
+
+
+# up to 128 rows for a KV head, and more; one line of key blocks, and one for each head
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("n_draft", [9, 40])
+def test_tree_wait_expires_and_writes_no_rows_of_other_calls(block, n_draft):
+    st = Store(T, 1, 32, 8, [20011, 37, 9000], 20064, block=block, seed=22)
+    try:
+        d = Drafts(st, 32, [n_draft, 3, n_draft], seed=22)
+        n = d.out.shape[0]
+        far = Drafts(st, 32, [50, 52, 60], seed=23)        # its shared units' rows lie behind n
+        ws = T.alloc_workspace(max(d.ws.numel(), far.ws.numel()))
+        far.ws = d.ws = ws
+        out = torch.full((256, 32, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((256, 32), 7.0, device="cuda")
+        d.out, d.lse = out[16: 16 + n], lse[16: 16 + n]
+        g = torch.Generator(device="cuda").manual_seed(24)
+        for held in ("another call's records", "anything"):
+            for _ in range(3):
+                far.run()
+                if held == "anything":
+                    ws.copy_(torch.randint(0, 256, ws.shape, generator=g, device="cuda", dtype=torch.uint8))
+                assert expire(d.run, ws)
+                for x in (out, lse):
+                    assert bool((x[:16] == 7.0).all()) and bool((x[16 + n:] == 7.0).all()), held
+        d.run()
+        d.check(heads=[0, 13, 31])
+        assert T.tria_read_device_status(ws) == 0
+    finally:
+        st.free()
