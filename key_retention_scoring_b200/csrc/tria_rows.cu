@@ -140,11 +140,11 @@ __global__ void __launch_bounds__(kMoveThreads, 6) commit_kernel(const __grid_co
           if (view_row(v, s, h, N + a, &from) && view_row(v, s, h, N + j, &to[u])) {
             xk[u] = *reinterpret_cast<const uint4 *>(kp + from);
             xv[u] = *reinterpret_cast<const uint4 *>(vp + from);
+            if (pos != nullptr) xp[u] = pos[(int64_t)h * v.max_seq_len + a];
             moves |= 1u << u;
           } else {
-            bad = true;
+            bad = true;  // neither the rows nor the position move
           }
-          if (pos != nullptr) xp[u] = pos[(int64_t)h * v.max_seq_len + a];
         }
       }
       j += step_j;
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kMoveThreads, 6) commit_kernel(const __grid_co
         if ((moves >> u) & 1u) {
           *reinterpret_cast<uint4 *>(kp + to[u]) = xk[u];
           *reinterpret_cast<uint4 *>(vp + to[u]) = xv[u];
+          if (pos != nullptr) pos[(int64_t)h * v.max_seq_len + j] = xp[u];
         }
-        if (pos != nullptr && first + u * kRowStep < rows && acc[j] > j) pos[(int64_t)h * v.max_seq_len + j] = xp[u];
         j += step_j;
         h += step_h;
         if (h >= hkv) {
