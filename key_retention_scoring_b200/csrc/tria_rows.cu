@@ -247,18 +247,18 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
   const int bs = v.block_size, bs_log2 = v.block_log2;
   const int b0 = paged ? t0 >> bs_log2 : 0, nb = paged ? ((t0 + nt - 1) >> bs_log2) - b0 + 1 : 1;
   __shared__ int64_t s_from[kForkBlocks], s_to[kForkDst][kForkBlocks];
-  __shared__ uint32_t s_need[kForkBlocks];
+  __shared__ uint32_t s_need[kForkBlocks], s_has[kForkBlocks];
   for (int d = d0; d < d1; d += kForkDst) {
     const int nd = min(kForkDst, d1 - d);
     __syncthreads();
     if (tid < nb) {
-      // where block b0 + tid of the source and of each destination begins, and
-      // which destinations need a copy of it
-      uint32_t need = 0;
+      // where block b0 + tid of the source and of each destination begins,
+      // which destinations need a copy of it, and which have the rows afterwards
+      uint32_t need = 0, has = 0;
       if (!paged) {
         s_from[0] = (int64_t)s * v.s_seq;
         for (int i = 0; i < nd; ++i) s_to[i][0] = (int64_t)p.dst[d + i] * v.s_seq;
-        need = (1u << nd) - 1u;
+        need = has = (1u << nd) - 1u;
       } else {
         const int sb = v.block_table[(int64_t)s * v.max_blocks + b0 + tid];
         const bool s_ok = sb >= 0 && sb < v.num_blocks;
@@ -269,14 +269,30 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
           const bool d_ok = db >= 0 && db < v.num_blocks;
           s_to[i][tid] = (int64_t)db * v.s_blk;
           bad = bad || !d_ok;
+          if (s_ok && d_ok) has |= 1u << i;
           if (s_ok && d_ok && db != sb) need |= 1u << i;
         }
         if (bad) atomicOr(p.status, 1);
       }
       s_need[tid] = need;
+      s_has[tid] = has;
     }
     // nothing to copy where every destination shares the chunk's blocks
-    if (!__syncthreads_or(tid < nb && s_need[tid] != 0)) continue;
+    const bool any = __syncthreads_or(tid < nb && s_need[tid] != 0) != 0;
+    const int t = tid % kForkRows;
+    if (!is_v && v.positions != nullptr && t < nt) {
+      // a position goes with its row, that of a shared block included
+      const uint32_t to = s_has[paged ? ((t0 + t) >> bs_log2) - b0 : 0];
+      const int64_t unit = (int64_t)v.hkv * v.max_seq_len;
+      int32_t *pos = v.positions + (int64_t)layer * unit + t0 + t;
+      for (int h = tid / kForkRows; h < v.hkv; h += kMoveThreads / kForkRows) {
+        int32_t *at = pos + (int64_t)h * v.max_seq_len;
+        const int32_t x = at[(int64_t)s * v.n_layers * unit];
+        for (int k = 0; k < nd; ++k)
+          if ((to >> k) & 1u) at[(int64_t)p.dst[d + k] * v.n_layers * unit] = x;
+      }
+    }
+    if (!any) continue;
     const int pieces = nt * v.hkv * kPieces;  // at most 64 x hkv x 16, 32 bits (host)
     for (int i0 = tid; i0 < pieces; i0 += kForkU * kMoveThreads) {
       uint4 x[kForkU];
@@ -303,17 +319,6 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
           if ((meta[u] >> k) & 1u)
             *reinterpret_cast<uint4 *>(base + s_to[k][meta[u] >> 8] + off[u]) = x[u];
     }
-  }
-  if (is_v || v.positions == nullptr) return;
-  const int64_t unit = (int64_t)v.hkv * v.max_seq_len;
-  const int32_t *from = v.positions + ((int64_t)s * v.n_layers + layer) * unit;
-  const int t = tid % kForkRows;
-  if (t >= nt) return;
-  for (int h = tid / kForkRows; h < v.hkv; h += kMoveThreads / kForkRows) {
-    const int64_t o = (int64_t)h * v.max_seq_len + t0 + t;
-    const int32_t x = from[o];
-    for (int d = d0; d < d1; ++d)
-      v.positions[((int64_t)p.dst[d] * v.n_layers + layer) * unit + o] = x;
   }
 }
 

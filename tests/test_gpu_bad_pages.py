@@ -13,7 +13,7 @@ if not torch.cuda.is_available():
 import key_retention_scoring_b200 as T  # noqa: E402
 from key_retention_scoring_b200 import build as tria_build  # noqa: E402
 from tests.serving_helpers import Store  # noqa: E402
-from tests.test_gpu_row_moves import Model, commit  # noqa: E402
+from tests.test_gpu_row_moves import Model, commit, fork  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -43,5 +43,31 @@ def test_commit_moves_a_position_only_with_its_row(page, bad_id, hkv):
             m.lens[s] += len(path)
         m.same()
         assert T.tria_read_device_status(ws) == 1
+    finally:
+        st.free()
+
+
+@pytest.mark.parametrize("hkv", [2, 8])
+@pytest.mark.parametrize("bad_id", [-1, 1 << 30])
+@pytest.mark.parametrize("who", ["source", "destination"])
+def test_fork_copies_a_position_only_with_its_row(who, bad_id, hkv):
+    # 40 destinations of 90 rows; block 5 is shared by all but the last two
+    n, kids = 90, 40
+    st = Store(T, 2, 8, hkv, [n] + [7] * kids, 112, block=16, seed=32, positions=True)
+    try:
+        st.table[1: kids - 1, 5] = st.table[0, 5]
+        bad = [0] if who == "source" else [1, 33, kids]
+        for s in bad:
+            st.table[s, 2] = bad_id
+        m = Model(st)
+        assert fork(st, [0] * kids, list(range(1, kids + 1))) == 1
+        for s in range(1, kids + 1):
+            for layer in range(2):
+                for t in range(n):
+                    if t // 16 != 2 or (s not in bad and 0 not in bad):
+                        m.move(layer, 0, t, s, t)
+                        m.move_pos(layer, 0, t, s, t)
+            m.lens[s] = n
+        m.same()
     finally:
         st.free()
