@@ -181,14 +181,15 @@ struct AtSmem {
 // ---------------------------------------------------------------------------
 // what a sequence holds, and the order of the work
 // ---------------------------------------------------------------------------
-// T, ctx and first row of sequence s; T = 0 for one that is empty or bad (*bad).
+// T, ctx and first row of sequence s; T = 0 for one that is empty or bad (*bad;
+// a cached length outside its range is bad with or without drafted tokens).
 template <int LAYOUT>
 __device__ __forceinline__ void seq_of(const AttendParams &p, int s, int &T, int &ctx, int64_t &row0, bool &bad) {
   const int64_t a = p.starts[s], b = p.starts[s + 1];
   const int n = LAYOUT != kPacked ? view_len(p.view, s, p.layer) : 0;  // read at the same time
   row0 = a;
   bad = a < 0 || b < a || b > p.n_tokens;
-  if (LAYOUT != kPacked && !bad && b > a)
+  if (LAYOUT != kPacked && !bad)
     bad = n < 0 || b - a > p.max_draft || b - a > p.view.max_seq_len - n;
   T = bad ? 0 : (int)(b - a);
   ctx = T > 0 ? n : 0;

@@ -1,5 +1,5 @@
-"""Pages outside the pool, in a cache with positions: a row and its position move
-together, or neither does (needs a B200)."""
+"""Pages and lengths that are out of range (needs a B200).  In a cache with
+positions a row and its position move together, or neither does."""
 from __future__ import annotations
 
 import pytest
@@ -14,6 +14,7 @@ import key_retention_scoring_b200 as T  # noqa: E402
 from key_retention_scoring_b200 import build as tria_build  # noqa: E402
 from tests.serving_helpers import Store  # noqa: E402
 from tests.test_gpu_row_moves import Model, commit, fork  # noqa: E402
+from tests.test_gpu_tree_attention import Drafts  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -69,5 +70,21 @@ def test_fork_copies_a_position_only_with_its_row(who, bad_id, hkv):
                         m.move_pos(layer, 0, t, s, t)
             m.lens[s] = n
         m.same()
+    finally:
+        st.free()
+
+
+@pytest.mark.parametrize("length", [-1, 129])
+@pytest.mark.parametrize("n_seq", [2, 40])
+def test_a_bad_length_is_flagged_without_drafted_tokens(length, n_seq):
+    st = Store(T, 1, 8, 2, [100] * n_seq, 128, seed=33)
+    try:
+        d = Drafts(st, 8, [3] * (n_seq - 1) + [0], seed=33)
+        d.run()
+        assert T.tria_read_device_status(d.ws) == 0
+        st.lens[n_seq - 1] = length          # the sequence that has no drafted tokens
+        d.run()
+        assert T.tria_read_device_status(d.ws) == 1
+        d.check(seqs=[0, n_seq - 2])
     finally:
         st.free()
