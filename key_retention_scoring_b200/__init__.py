@@ -451,11 +451,12 @@ def _stream_on(stream, dev):
 
 def _row_strides(strides, n, h):
     """(token, head) strides of [n tokens, h heads, 128]; a dimension of one
-    entry never advances, so any stride stands for it."""
+    entry never advances, so its own stride is not looked at."""
     st, sh, _ = strides
     if n > 1 and h > 1:
         return st, sh
-    return (st if n > 1 else max(st, sh * h, 128), sh if h > 1 else 128)
+    sh = sh if h > 1 else 128
+    return st if n > 1 else sh * h, sh
 
 
 def tria_set_attention_wait_limit(ns: int):

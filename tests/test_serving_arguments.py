@@ -18,3 +18,11 @@ def test_wait_limit_refuses_negative_bounds():
     assert e.value.status == 1
     T.tria_set_attention_wait_limit(2 ** 63 - 1)
     T.tria_set_attention_wait_limit(0)
+
+
+@pytest.mark.parametrize("shape,strides,want", [
+    ((5, 8), (1024, 128, 1), (1024, 128)), ((5, 1), (1024, 77, 1), (1024, 128)), ((1, 8), (1028, 128, 1), (1024, 128)),
+    ((1, 8), (3, 256, 1), (2048, 256)), ((1, 1), (1028, 131, 1), (128, 128)), ((0, 8), (0, 128, 1), (1024, 128)),
+    ((1, 8), (1028, 4, 1), (32, 4))], ids=str)
+def test_strides_of_one_entry_dimensions_are_not_looked_at(shape, strides, want):
+    assert T._row_strides(strides, *shape) == want
