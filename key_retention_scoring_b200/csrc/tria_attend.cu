@@ -61,8 +61,7 @@ using namespace tc;
 // Waits of the pipeline: the threads sleep in the barrier unit (polling took
 // shared-memory cycles from the products: 1.25 times the time); the clock and
 // the abort flag are looked at after a sleep that ran out.  The limit counts
-// SM cycles at 2 GHz, which is never short; with the global timer in its place,
-// calls that ran their usual time were now and then reported as expired.
+// SM cycles at 2 GHz, which is never short and does not step back (time_over).
 __device__ __forceinline__ bool poll_on(uint32_t bar, uint32_t parity, const WaitCtl &w) {
   const long long t0 = clock64();
   for (;;) {

@@ -237,6 +237,13 @@ tria_status check_header_workspace(void *ws, size_t have, size_t need);
 bool encode_rows_map(CUtensorMap *map, const void *base, const uint64_t (&dims)[4],
                      const int64_t (&strides)[3], const uint32_t (&box)[4]);
 
+// Whether more than limit_ns (at most 2^63 - 1) lie between two readings of
+// %globaltimer.  The second may be a tick below the first (the timer was seen to
+// step back): the difference is signed, or such a step would read as 584 years.
+__host__ __device__ __forceinline__ bool time_over(uint64_t t0, uint64_t now, uint64_t limit_ns) {
+  return (int64_t)(now - t0) > (int64_t)limit_ns;
+}
+
 constexpr size_t kHeaderBytes = 256;  // workspace header; status flags at byte 4
 
 // N of (s, layer), or -1 when it lies outside [0, max_seq_len]

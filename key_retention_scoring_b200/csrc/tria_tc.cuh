@@ -137,7 +137,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
   for (;;) {
     if (mbar_try_sleep(a, parity, w.hint_ns)) return true;
     if (*w.abort_flag) return false;
-    if (global_timer() - t0 > w.limit_ns) {
+    if (time_over(t0, global_timer(), w.limit_ns)) {
       flag_expiry(w);
       return false;
     }
@@ -151,7 +151,7 @@ __device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, int32
   const uint64_t t0 = global_timer();
   for (;;) {
     if (mbar_try_sleep(a, parity, kSuspendNs)) return true;
-    if (global_timer() - t0 > kDrainNs) {
+    if (time_over(t0, global_timer(), kDrainNs)) {
       atomicOr(status, 2);
       return false;
     }
@@ -168,7 +168,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
   for (;;) {
     if (__all_sync(kFull, mbar_try_sleep(a, parity, w.hint_ns))) return true;
     if (__any_sync(kFull, *w.abort_flag != 0)) return false;
-    if (__any_sync(kFull, global_timer() - t0 > w.limit_ns)) {
+    if (__any_sync(kFull, time_over(t0, global_timer(), w.limit_ns))) {
       if (lane == 0) flag_expiry(w);
       return false;
     }
