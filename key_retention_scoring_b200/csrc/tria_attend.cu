@@ -1465,7 +1465,7 @@ cudaError_t launch_attend(const AttendParams &p, int grid, cudaStream_t st) {
 // Tiles of rows per (sequence, KV head) at most, and rows of a partial.
 struct TreeShape {
   bool dualk;
-  int rows, tiles, grid;
+  int rows, tiles, grid, sms;
 };
 
 tria_status tree_shape(const tria_model_desc &d, const tria_cache_view *c, int max_draft, TreeShape *sh) {
@@ -1480,6 +1480,7 @@ tria_status tree_shape(const tria_model_desc &d, const tria_cache_view *c, int m
   sh->tiles = (int)(((int64_t)max_draft * g + sh->rows - 1) / sh->rows);
   const int64_t blocks = (int64_t)c->n_seq * d.n_kv_heads * sh->tiles * ((c->max_seq_len + (int64_t)kBN - 1) / kBN);
   sh->grid = blocks < sms ? (int)blocks : sms;
+  sh->sms = sms;
   return TRIA_OK;
 }
 
@@ -1496,7 +1497,8 @@ cudaError_t launch_tree(const AttendParams &p, const TreeShape &sh, cudaStream_t
   const int64_t all = (int64_t)p.n_seq * p.hkv * sh.tiles;
   const int64_t units = all < sh.grid ? all : sh.grid;  // no more shared ones than CTAs
   int64_t y = 32 * ((rows + 31) / 32) / kCombineWarps;
-  if (y > 4 * 148 / units) y = 4 * 148 / units > 0 ? 4 * 148 / units : 1;
+  const int64_t resident = 4 * (int64_t)sh.sms / units;
+  if (y > resident) y = resident > 0 ? resident : 1;
   const dim3 grid((unsigned)units, (unsigned)y);
   return launch_early(combine_kernel<AtCfg<DUALK>::ROWS>, grid, 32 * kCombineWarps, 0, st, p, sh.grid);
 }
