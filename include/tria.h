@@ -539,7 +539,9 @@ tria_status tria_set_attention_wait_limit(int64_t ns);
  * that may overlap need separate workspaces.
  * The result does not depend on how the work is spread: equal inputs give
  * equal bits.  Errors: INVALID_ARG, UNSUPPORTED (head_dim != 128, G not a
- * power of two up to 16, strides a tensor map cannot express), WORKSPACE, CUDA.
+ * power of two up to 16, strides a tensor map cannot express; every call, where
+ * the compiler that built the library did not give the kernel the 168 registers
+ * a thread that its register split counts on), WORKSPACE, CUDA.
  */
 tria_status tria_prompt_workspace_size(const tria_model_desc *desc, int n_seq, size_t *bytes);
 tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q,
@@ -587,7 +589,7 @@ tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q,
  * Workspace: tria_tree_workspace_size bytes (256-byte aligned); status flags
  * as in tria_prompt_attention.  Calls that may overlap need separate
  * workspaces.  Equal inputs give equal bits.
- * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (as tria_prompt_attention), WORKSPACE, CUDA.
  */
 tria_status tria_tree_workspace_size(const tria_stats *stats, const tria_cache_view *cache,
                                      int max_draft, size_t *bytes);
@@ -648,7 +650,8 @@ tria_status tria_tree_commit(const tria_stats *stats, const tria_cache_view *cac
  * outside [0, num_blocks) in either row sets status bit 0 and its rows are not
  * copied.  Rows of dst from N on are left as they are.  query_pos is not used.
  * Workspace: tria_fork_workspace_size bytes (256-byte aligned): the status
- * flags.  Errors: INVALID_ARG, WORKSPACE, CUDA.
+ * flags.  Errors: INVALID_ARG, UNSUPPORTED (more than 2097149 KV
+ * heads), WORKSPACE, CUDA.
  */
 tria_status tria_fork_workspace_size(const tria_stats *stats, const tria_cache_view *cache,
                                      size_t *bytes);

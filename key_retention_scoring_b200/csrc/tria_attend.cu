@@ -1453,13 +1453,18 @@ cudaError_t launch_attend(const AttendParams &p, int grid, cudaStream_t st) {
   if (attr_dev != dev) {
     e = cudaFuncSetAttribute(attend_kernel<DUALK, LAYOUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    // the register split draws on what the block is launched with
+    // The register split draws on what the block is launched with: where a compiler
+    // gave the kernel another count, a group would wait for registers for good.
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, attend_kernel<DUALK, LAYOUT>)) != cudaSuccess) return e;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
     attr_dev = dev;
   }
   return launch_early(attend_kernel<DUALK, LAYOUT>, dim3((unsigned)grid), kAtThreads, smem, st, p);
+}
+
+tria_status launch_status(cudaError_t e) {
+  return e == cudaSuccess ? TRIA_OK : e == cudaErrorNotSupported ? TRIA_ERR_UNSUPPORTED : TRIA_ERR_CUDA;
 }
 
 // Tiles of rows per (sequence, KV head) at most, and rows of a partial.
@@ -1551,8 +1556,7 @@ tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q, in
   // at most one item per tile of rows and KV head, the sequences' last tiles part full
   const int64_t tiles = (n_tokens * p.g + AtCfg<false>::ROWS - 1) / AtCfg<false>::ROWS + n_seq;
   const int grid = (int)(tiles * p.hkv < sms ? tiles * p.hkv : sms);
-  const cudaError_t e = launch_attend<false, kPacked>(p, grid, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+  return launch_status(launch_attend<false, kPacked>(p, grid, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 tria_status tria_tree_workspace_size(const tria_stats *stats, const tria_cache_view *cache, int max_draft,
@@ -1606,7 +1610,7 @@ tria_status tria_tree_attention(const tria_stats *stats, const tria_cache_view *
   else
     e = sh.dualk ? launch_tree<true, TRIA_LAYOUT_CONTIGUOUS>(p, sh, cs)
                  : launch_tree<false, TRIA_LAYOUT_CONTIGUOUS>(p, sh, cs);
-  return e == cudaSuccess ? TRIA_OK : TRIA_ERR_CUDA;
+  return launch_status(e);
 }
 
 }  // extern "C"
