@@ -8,6 +8,7 @@ tria_score, tria_select, tria_compact, tria_compress_pass, ...
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -583,6 +584,15 @@ def tria_fork_workspace_size(stats, cache) -> int:
     return out.value
 
 
+def _indices(where, name, x):
+    """A sequence of whole numbers as C ints; fractions and numbers past 32 bits
+    are refused rather than taken for other indices."""
+    try:
+        return array.array("i", x.tolist() if hasattr(x, "tolist") else list(x))
+    except (TypeError, OverflowError):
+        raise TriaError(1, f"{where}: {name} must be a sequence of 32-bit indices") from None
+
+
 def tria_fork_sequences(stats, cache, src, dst, layer0, layer1, workspace, stream=None):
     """Copy sequence src[i] to sequence dst[i] (host sequences of indices) in
     layers [layer0, layer1): rows, positions and length; paged blocks that both
@@ -593,11 +603,11 @@ def tria_fork_sequences(stats, cache, src, dst, layer0, layer1, workspace, strea
     if not (workspace.dtype is torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous()
             and dev >= 0 and dev == torch.cuda.current_device()):
         _refuse(where, ("workspace", workspace, (torch.uint8,), (None,), True))
-    if len(src) != len(dst):
+    a, b = _indices(where, "src", src), _indices(where, "dst", dst)
+    if len(a) != len(b):
         raise TriaError(1, f"{where}: src and dst must have the same length")
-    a, b = (np.ascontiguousarray(x, dtype=np.int32) for x in (src, dst))
-    _check(lib().tria_fork_sequences(stats.handle, ctypes.byref(cache.view), a.ctypes.data,
-                                     b.ctypes.data, len(a), layer0, layer1, workspace.data_ptr(),
+    _check(lib().tria_fork_sequences(stats.handle, ctypes.byref(cache.view), a.buffer_info()[0],
+                                     b.buffer_info()[0], len(a), layer0, layer1, workspace.data_ptr(),
                                      workspace.numel(), _stream_on(stream, dev)), where)
 
 

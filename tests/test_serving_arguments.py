@@ -1,10 +1,11 @@
 """Arguments of the serving operators that the host looks at alone (no GPU)."""
+import numpy as np
 import pytest
 
 import key_retention_scoring_b200 as T
 from key_retention_scoring_b200 import build as tria_build
 
-pytest.importorskip("torch")
+torch = pytest.importorskip("torch")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -26,3 +27,17 @@ def test_wait_limit_refuses_negative_bounds():
     ((1, 8), (1028, 4, 1), (32, 4))], ids=str)
 def test_strides_of_one_entry_dimensions_are_not_looked_at(shape, strides, want):
     assert T._row_strides(strides, *shape) == want
+
+
+@pytest.mark.parametrize("x", [[], (), [0, 3], (2,), np.array([1, 2]), np.array([5], np.uint8), torch.tensor([4, 1])], ids=str)
+def test_fork_indices(x):
+    got = T._indices("here", "src", x)
+    assert got.typecode == "i" and got.itemsize == 4 and got.tolist() == [int(v) for v in x]
+
+
+@pytest.mark.parametrize("x", [[0.9], [2 ** 32 + 1], np.array([2 ** 32 + 1]), np.array([-2 ** 31 - 1]), np.array([2 ** 64 - 1], np.uint64),
+                               [[0, 1]], 3, "12", ["1"], [None], torch.tensor([1.0])], ids=str)
+def test_fork_refuses_what_is_no_index(x):
+    with pytest.raises(T.TriaError) as e:
+        T._indices("here", "src", x)
+    assert e.value.status == 1
