@@ -533,7 +533,8 @@ tria_status tria_set_attention_wait_limit(int64_t ns);
  * Rows of no sequence (before seq_starts[0], behind seq_starts[n_seq]) are
  * left as they are in out and lse, and what q, k, v hold there has no effect.
  * A row depends on the rows j <= i of its sequence alone: infinities and NaN
- * in later rows or in other sequences do not reach it.
+ * in later rows or in other sequences do not reach it.  A row whose logits are
+ * all -inf has no softmax: out NaN, lse -inf.
  * Workspace: tria_prompt_workspace_size bytes (256-byte aligned); its first
  * 256 bytes hold the status flags read by tria_read_device_status.  Calls
  * that may overlap need separate workspaces.
@@ -579,7 +580,7 @@ tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q,
  *   out     device bf16 [n_tokens][n_q_heads][128] (16-byte aligned, contiguous)
  *   lse     optional device fp32 [n_tokens][n_q_heads] (natural log)
  * A token that may attend to nothing (N = 0, mask 0) gets out = 0 and
- * lse = -inf.  Rows outside a token's set do not reach its output, whatever
+ * lse = -inf; one whose logits are all -inf, out NaN and lse -inf.  Rows outside a token's set do not reach its output, whatever
  * they hold.  A sequence with a bad pair of starts, T_s > max_draft, N outside
  * [0, max_seq_len] or N + T_s > max_seq_len sets status bit 0 and is skipped
  * (its rows are left as they are).  Paged block ids outside [0, num_blocks)

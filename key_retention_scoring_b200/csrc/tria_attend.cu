@@ -865,6 +865,15 @@ __device__ __forceinline__ bool step_masked(const AttendParams &p, const Item &x
   return p.mask != nullptr ? k0 + kHN > x.ctx : k0 + kHN - 1 > x.ctx + x.tok0;
 }
 
+// Whether this row may see any key at all (asked where all its logits were -inf).
+__device__ __noinline__ bool sees_any(const AttendParams &p, const Item &x, int tok) {
+  if (tok >= x.T) return false;
+  if (x.ctx > 0 || p.mask == nullptr) return true;
+  uint32_t any = 0;
+  for (int k0 = 0; k0 < x.T; k0 += 32) any |= sees(p, x, tok, k0);
+  return any != 0;
+}
+
 // v_j that are not finite, of the masked steps' keys that this row sees, added to o (dims d0 .. d0 + 31).
 template <int LAYOUT>
 __device__ __noinline__ void add_not_finite(const AttendParams &p, const Item &x, int tok, int d0, float (&o)[32]) {
@@ -926,6 +935,13 @@ template <int ROWS>
 __device__ __forceinline__ int64_t part_at(int slot, int row, int d4) {
   return ((int64_t)slot * 32 + d4) * ROWS + row;
 }
+
+// A row's l where it sees keys and all its logits are -inf: such a row has no
+// softmax (0 / 0).  0 is a row that sees no key.
+constexpr float kNoWeight = -1.f;
+
+__device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN; }
+__device__ __forceinline__ float log_sum(float m, float l) { return l <= 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
 // One step of transposing 4 x 4 pieces of 4 words over 4 lanes: lanes MASK apart
 // swap the pieces that lie WORDS apart.
@@ -1112,7 +1128,13 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
     if (!idle) {
       const bool poisoned = sm.poison[it & 3] == it + 1;
       const bool mine_row = tok < x.T;
-      const float inv = x.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      // no logit above -inf (and none is NaN): l is what the FMA pipe's floor left
+      if (m == -INFINITY && l == l) {
+        const Item z = x;
+        l = sees_any(p, z, tok) ? kNoWeight : 0.f;
+      }
+      __syncwarp();  // the reads of O below are the whole warp's
+      const float inv = x.slot >= 0 ? 1.f : inverse(l);
       const int row = (DUALK ? 0 : 128 * t) + r;
       const int64_t orow = (x.row0 + tok) * p.hq + ((int64_t)x.h << p.g_log2) + (r & (p.g - 1));
       constexpr int kChunks = DUALK ? 2 : 4;  // DUALK: each group takes 64 of the dims
@@ -1172,7 +1194,7 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
         if (x.slot >= 0)
           *reinterpret_cast<float2 *>(p.part_ml + ((int64_t)x.slot * Cfg::ROWS + row) * 2) = make_float2(m, l);
         else if (p.lse != nullptr)
-          p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          p.lse[orow] = log_sum(m, l);
       }
     }
     tc_fence_before();
@@ -1304,6 +1326,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __
     // partial c: 0 is the first CTA's
     auto slot = [&](int c) { return c == 0 ? u.first : u.next + (c - 1) * u.step; };
     float M = -INFINITY, L = 0.f;
+    bool none = false;  // a part says that the row sees keys (the L of such a part has no weight)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b = 0; b <= u.count; b += kBatch) {
       const int n = min(kBatch, u.count + 1 - b);
@@ -1332,17 +1355,19 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __
       for (int c = 0; c < kBatch; ++c) {
         const float f = ml[c].x == -INFINITY ? 0.f : ex2(ml[c].x - M);
         L = fmaf(f, ml[c].y, L);
+        none = none || ml[c].y == kNoWeight;
         acc.x = fmaf(f, o[c].x, acc.x);
         acc.y = fmaf(f, o[c].y, acc.y);
         acc.z = fmaf(f, o[c].z, acc.z);
         acc.w = fmaf(f, o[c].w, acc.w);
       }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    if (L == 0.f && none) L = kNoWeight;
+    const float inv = inverse(L);
     const int64_t orow = (u.row0 + (r >> p.g_log2)) * p.hq + ((int64_t)u.h << p.g_log2) + (r & (p.g - 1));
     *reinterpret_cast<uint2 *>(p.out + orow * 128 + 4 * d4) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (p.lse != nullptr && d4 == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (p.lse != nullptr && d4 == 0) p.lse[orow] = log_sum(M, L);
   }
 }
 
