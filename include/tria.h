@@ -526,15 +526,17 @@ tria_status tria_set_attention_wait_limit(int64_t ns);
  *   seq_starts  device int32 [n_seq + 1], non-decreasing in [0, n_tokens].  A
  *               sequence with a bad pair of starts sets status bit 0 and is
  *               skipped; empty sequences are allowed.
- *   scale   softmax scale, finite and > 0
+ *   scale   softmax scale, > 0, at most 2.35e38
  *   out     device bf16 [n_tokens][n_q_heads][128] (16-byte aligned,
  *           contiguous): sums in fp32, rounded once.  May not overlap q, k, v.
  *   lse     optional device fp32 [n_tokens][n_q_heads] (natural log)
  * Rows of no sequence (before seq_starts[0], behind seq_starts[n_seq]) are
  * left as they are in out and lse, and what q, k, v hold there has no effect.
  * A row depends on the rows j <= i of its sequence alone: infinities and NaN
- * in later rows or in other sequences do not reach it.  A row whose logits are
- * all -inf has no softmax: out NaN, lse -inf.
+ * in later rows or in other sequences do not reach it.
+ * Logits are taken between -2^30 ln 2 and 2^30 ln 2 (7.4e8).  One below has no
+ * weight, as -inf has none; a row that has only such logits has no softmax: out
+ * NaN, lse -inf.  A row with a logit above, +inf or NaN has out and lse NaN.
  * Workspace: tria_prompt_workspace_size bytes (256-byte aligned); its first
  * 256 bytes hold the status flags read by tria_read_device_status.  Calls
  * that may overlap need separate workspaces.
@@ -576,11 +578,11 @@ tria_status tria_prompt_attention(const tria_model_desc *desc, const void *q,
  *           ancestors and the token itself; any set is allowed; bits from T_s
  *           on have no effect).  NULL: a chain, the drafted rows <= i
  *           (mask_words is not read).
- *   scale   softmax scale, finite and > 0
+ *   scale   softmax scale, > 0, at most 2.35e38
  *   out     device bf16 [n_tokens][n_q_heads][128] (16-byte aligned, contiguous)
  *   lse     optional device fp32 [n_tokens][n_q_heads] (natural log)
  * A token that may attend to nothing (N = 0, mask 0) gets out = 0 and
- * lse = -inf; one whose logits are all -inf, out NaN and lse -inf.  Rows outside a token's set do not reach its output, whatever
+ * lse = -inf.  The range of the logits is that of tria_prompt_attention.  Rows outside a token's set do not reach its output, whatever
  * they hold.  A sequence with a bad pair of starts, T_s > max_draft, N outside
  * [0, max_seq_len] or N + T_s > max_seq_len sets status bit 0 and is skipped
  * (its rows are left as they are).  Paged block ids outside [0, num_blocks)

@@ -106,6 +106,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // more than this, so most steps leave O in tensor memory alone; weights stay
 // below 2^8, well inside fp32 and bf16.
 constexpr float kSlack = 8.f;
+// Range of the running maximum.  It is rounded, by up to 64 at 2^30, and all weights
+// of the row are off by that factor, which fp32 holds; further out they would
+// overflow or vanish.  So it begins at -2^30, logits below have no weight (-inf of
+// masked places among them), and one above 2^30 makes its row NaN.
+constexpr float kLowest = -1073741824.f;
 // Of every 8 pairs of exponentials this many run on the FMA pipe, the rest on the
 // special-function unit (16384-token prompt, 64 query heads: 0, 1, 2, 3 of 8 took
 // 3779, 3719, 3870, 3800 us).
@@ -865,7 +870,7 @@ __device__ __forceinline__ bool step_masked(const AttendParams &p, const Item &x
   return p.mask != nullptr ? k0 + kHN > x.ctx : k0 + kHN - 1 > x.ctx + x.tok0;
 }
 
-// Whether this row may see any key at all (asked where all its logits were -inf).
+// Whether this row may see any key at all (asked where no logit had weight).
 __device__ __noinline__ bool sees_any(const AttendParams &p, const Item &x, int tok) {
   if (tok >= x.T) return false;
   if (x.ctx > 0 || p.mask == nullptr) return true;
@@ -936,9 +941,13 @@ __device__ __forceinline__ int64_t part_at(int slot, int row, int d4) {
   return ((int64_t)slot * 32 + d4) * ROWS + row;
 }
 
-// A row's l where it sees keys and all its logits are -inf: such a row has no
-// softmax (0 / 0).  0 is a row that sees no key.
+// A row's l where it sees keys, none with weight: such a row has no softmax (0 / 0).
+// 0 is a row that sees no key.
 constexpr float kNoWeight = -1.f;
+
+// l of a row at the end: what its weights summed to at kLowest is the FMA pipe's
+// floor (a NaN stays).
+__device__ __forceinline__ float weight_sum(float m, float l) { return m == kLowest && l == l ? 0.f : l; }
 
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN; }
 __device__ __forceinline__ float log_sum(float m, float l) { return l <= 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
@@ -978,7 +987,7 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
     const int first_tok = x.tok0 + (DUALK ? 0 : t * (kRows >> p.g_log2));
     const int tok = first_tok + (r >> p.g_log2);
     const bool idle = first_tok + ((w * 32) >> p.g_log2) >= x.T;  // no row of this warp is one of the sequence
-    float m = -INFINITY, l = 0.f;
+    float m = kLowest, l = 0.f;
     // The softmax of step g.  Steps with masked places come last and have code of
     // their own: one loop for both took 1.25 times as long, masked or not.
     auto step = [&](auto is_masked, int g) -> bool {
@@ -1041,10 +1050,9 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
           l *= a;
           if (g > 0 && !rescale(to, a, &sm.o_done[t], (uint32_t)((od[t] + g - 1) & 1), wc)) return false;
         }
-        // a NaN or +inf logit makes the row NaN, whichever way its exponential is taken
-        if (!(top < INFINITY)) l = NAN;
-        const float mu = m == -INFINITY ? 0.f : -m;
-        const f32x2 mu2 = pair(mu, mu), qs2 = pair(qs, qs);
+        // a NaN, +inf or too large logit makes the row NaN, whichever way its exponential is taken
+        if (!(top <= -kLowest)) l = NAN;
+        const f32x2 mu2 = pair(-m, -m), qs2 = pair(qs, qs);
         // of every 8 pairs of weights, the first `fma` go to the FMA pipe
         auto weights = [&](int fma) {
 #pragma unroll
@@ -1105,14 +1113,14 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
     float f0 = 1.f, f1 = 0.f;  // DUALK: factors of the two halves' O
     if (DUALK) {
       sm.ml[t][0][r] = m;
-      sm.ml[t][1][r] = l;
+      sm.ml[t][1][r] = weight_sum(m, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ml_full);
       if (!warp_poll(&sm.ml_full, (uint32_t)(it & 1), wc)) return;
       const float m0 = sm.ml[0][0][r], m1 = sm.ml[1][0][r];
       m = fmaxf(m0, m1);
-      f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
-      f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+      f0 = ex2(m0 - m);
+      f1 = ex2(m1 - m);
       l = sm.ml[0][1][r] * f0 + sm.ml[1][1][r] * f1;
     }
     // the last product of this half (DUALK: of both) must have been added to O
@@ -1128,10 +1136,10 @@ __device__ void soft_role(const AttendParams &p, AtSmem<DUALK> &sm, uint32_t tme
     if (!idle) {
       const bool poisoned = sm.poison[it & 3] == it + 1;
       const bool mine_row = tok < x.T;
-      // no logit above -inf (and none is NaN): l is what the FMA pipe's floor left
-      if (m == -INFINITY && l == l) {
+      l = weight_sum(m, l);
+      if (l == 0.f) {
         const Item z = x;
-        l = sees_any(p, z, tok) ? kNoWeight : 0.f;
+        if (sees_any(p, z, tok)) l = kNoWeight;
       }
       __syncwarp();  // the reads of O below are the whole warp's
       const float inv = x.slot >= 0 ? 1.f : inverse(l);
@@ -1325,7 +1333,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __
     if (r >= u.rows) continue;
     // partial c: 0 is the first CTA's
     auto slot = [&](int c) { return c == 0 ? u.first : u.next + (c - 1) * u.step; };
-    float M = -INFINITY, L = 0.f;
+    float M = kLowest, L = 0.f;
     bool none = false;  // a part says that the row sees keys (the L of such a part has no weight)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b = 0; b <= u.count; b += kBatch) {
@@ -1334,7 +1342,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __
       float2 ml[kBatch];
 #pragma unroll
       for (int c = 0; c < kBatch; ++c) {
-        ml[c] = make_float2(-INFINITY, 0.f);
+        ml[c] = make_float2(kLowest, 0.f);
         o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c < n) {
           o[c] = __ldcg(reinterpret_cast<const float4 *>(p.part_o) + part_at<ROWS>(slot(b + c), r, d4));
@@ -1344,7 +1352,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __
       float top = M;
 #pragma unroll
       for (int c = 0; c < kBatch; ++c) top = fmaxf(top, ml[c].x);
-      const float back = M == -INFINITY ? 0.f : ex2(M - top);
+      const float back = ex2(M - top);
       M = top;
       L *= back;
       acc.x *= back;
@@ -1353,9 +1361,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const __
       acc.w *= back;
 #pragma unroll
       for (int c = 0; c < kBatch; ++c) {
-        const float f = ml[c].x == -INFINITY ? 0.f : ex2(ml[c].x - M);
-        L = fmaf(f, ml[c].y, L);
-        none = none || ml[c].y == kNoWeight;
+        const float f = ex2(ml[c].x - M);
+        const bool empty = ml[c].y == kNoWeight;
+        none = none || empty;
+        L = fmaf(f, empty ? 0.f : ml[c].y, L);
         acc.x = fmaf(f, o[c].x, acc.x);
         acc.y = fmaf(f, o[c].y, acc.y);
         acc.z = fmaf(f, o[c].z, acc.z);
@@ -1389,10 +1398,12 @@ tria_status check_desc(const tria_model_desc &d) {
   return TRIA_OK;
 }
 
+float base2(float scale) { return (float)((double)scale * 1.4426950408889634); }
+
 // What both operators ask of the queries and the outputs.
 tria_status check_rows(const void *q, int64_t q_tok, int64_t q_head, int64_t n_tokens,
                        const int32_t *starts, float scale, const void *out, const float *lse) {
-  if (n_tokens < 0 || n_tokens > INT32_MAX - 1024 || !std::isfinite(scale) || !(scale > 0.f)) return TRIA_ERR_INVALID_ARG;
+  if (n_tokens < 0 || n_tokens > INT32_MAX - 1024 || !(scale > 0.f) || !std::isfinite(base2(scale))) return TRIA_ERR_INVALID_ARG;
   if (!strides_ok(q_tok, q_head) || starts == nullptr || !aligned(starts, 4)) return TRIA_ERR_INVALID_ARG;
   if (n_tokens > 0 && (q == nullptr || out == nullptr)) return TRIA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return TRIA_ERR_INVALID_ARG;
@@ -1408,7 +1419,7 @@ void fill_rows(AttendParams &p, const tria_model_desc &d, int n_seq, int64_t n_t
   for (p.g_log2 = 0; (1 << p.g_log2) < p.g; ++p.g_log2) {}
   p.n_tokens = n_tokens;
   p.starts = starts;
-  p.qscale = (float)((double)scale * 1.4426950408889634);
+  p.qscale = base2(scale);
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
   p.status = reinterpret_cast<int32_t *>(static_cast<unsigned char *>(ws) + 4);

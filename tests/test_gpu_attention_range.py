@@ -95,3 +95,87 @@ def test_keys_whose_logits_are_minus_infinity_have_no_weight(n_draft):
             check(d.out[:, h], d.lse[:, h], attend(d.q[:, h], k, v, sees), h)
     finally:
         st.free()
+
+
+# Logits that are exact in fp32 (products of bf16 numbers in one or two dims), so that
+# the tolerance is that of the softmax alone: weights within 2^-8 + 2^-13 (P in bf16,
+# the exponential), the output rounded to bf16 (2^-8); lse = RN(RN(max qs) + log2 l) ln 2
+# with qs and ln 2 within 2^-25 of theirs and three roundings of 2^-24: within 2^-21.
+def far_rows(kind, n, e, sign, gen):
+    """[n] and [n] of a key's first two dims, and of a query's, scaled to 2^e."""
+    a, b = 2.0 ** (e // 2), 2.0 ** (e - e // 2)
+    j = torch.arange(n, device="cuda", dtype=torch.float64)
+    zero = torch.zeros(n, device="cuda", dtype=torch.float64)
+    if kind == "ties":          # equal to the largest, a step of bf16 below it, far below it
+        off = torch.tensor([0, 0, 1, 2, 60], device="cuda")[torch.randint(0, 5, (n,), generator=gen, device="cuda")]
+        return b * (sign - 2.0 ** -7 * off), zero, a, 0.0
+    if kind == "rising":        # from 1 to 2^e in size, the largest last
+        return torch.sort(sign * torch.exp2(j * (e / (n - 1)))).values, zero, 1.0, 0.0
+    if kind == "falling":
+        return torch.sort(sign * torch.exp2(j * (e / (n - 1))), descending=True).values, zero, 1.0, 0.0
+    small = torch.randint(-24, 25, (n,), generator=gen, device="cuda").double() * 0.125   # "near": 2^e and a little
+    return sign * b + zero, small, a, 1.0
+
+
+FAR = [("ties", e, s) for e in (20, 28, 31, 32, 40, 100) for s in (1, -1)] + [
+    (k, e, s) for k in ("rising", "falling") for e in (28, 33, 60, 110) for s in (1, -1)] + [("near", 20, 1), ("near", 20, -1)]
+LIMIT = 2.0 ** 30 * 0.6931471805599453
+
+
+def fill_far(k, q, kind, e, sign, seed):
+    """k [n, heads, 128], q [m, heads, 128] in place."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    k.zero_()
+    q.zero_()
+    for h in range(k.shape[1]):
+        k0, k1, q0, q1 = far_rows(kind, k.shape[0], e, sign, gen)
+        k[:, h, 0], k[:, h, 1] = k0.to(k.dtype), k1.to(k.dtype)
+    q[:, :, 0], q[:, :, 1] = q0, q1
+
+
+def check_exact(out, lse, q, k, v, allowed, where):
+    """Rows within the range against the formula, the others as they are documented.
+    No row's largest logit is so near the range's ends that its roundings decide."""
+    z = torch.where(allowed, q.double() @ k.double().T, -INF)
+    top = z.amax(1)
+    assert not bool(((top.abs() / LIMIT - 1.0).abs() < 2.0 ** -20).any())
+    above, below = top > LIMIT, top < -LIMIT
+    assert bool(torch.isnan(out[above | below].float()).all())
+    assert bool(torch.isnan(lse[above]).all()) and bool((lse[below] == -INF).all())
+    z, out, lse = (x[~(above | below)] for x in (z, out, lse))
+    if z.shape[0] == 0:
+        return
+    ref = torch.logsumexp(z, 1)
+    w = torch.exp(z - z.amax(1, keepdim=True))
+    w = w / w.sum(1, keepdim=True)
+    want = w @ v.double()
+    moved = (w @ v.double().abs()) * (2.0 ** -8 + 2.0 ** -13)
+    d = (out.double() - want).abs()
+    assert bool((d <= moved + 2.0 ** -8 * (want.abs() + moved)).all()), (where, float(d.max()))
+    assert bool(((lse.double() - ref).abs() <= 2.0 ** -21 * ref.abs() + 2e-5).all()), where
+
+
+@pytest.mark.parametrize("kind,e,sign", FAR)
+def test_prompt_logits_far_from_zero(kind, e, sign):
+    p = Prompt(4, 2, [400], seed=54)
+    fill_far(p.k, p.q, kind, e, sign, 55)
+    p.run(scale=1.0)
+    for h in range(4):
+        check_exact(p.out[:, h], p.lse[:, h], p.q[:, h], p.k[:, h // 2], p.v[:, h // 2], causal(400), h)
+
+
+@pytest.mark.parametrize("n_draft", [5, 40])
+@pytest.mark.parametrize("kind,e,sign", FAR)
+def test_tree_logits_far_from_zero(kind, e, sign, n_draft):
+    n = 8000
+    st = Store(T, 1, 16, 2, [n], n + n_draft, seed=56)
+    try:
+        d = Drafts(st, 16, [n_draft], seed=56)
+        fill_far(st.k[0, 0].transpose(0, 1), d.q, kind, e, sign, 57)
+        d.run(scale=1.0)
+        sees = draft_sees(n, n_draft, d.mask)
+        for h in (0, 7, 8):
+            k, v = (st.rows(x, 0, 0, h // 8, n + n_draft) for x in (st.k, st.v))
+            check_exact(d.out[:, h], d.lse[:, h], d.q[:, h], k, v, sees, h)
+    finally:
+        st.free()

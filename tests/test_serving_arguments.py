@@ -1,4 +1,6 @@
 """Arguments of the serving operators that the host looks at alone (no GPU)."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -41,3 +43,10 @@ def test_fork_refuses_what_is_no_index(x):
     with pytest.raises(T.TriaError) as e:
         T._indices("here", "src", x)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("scale,status", [(2.35e38, 0), (2.4e38, 1), (3.4e38, 1), (1e-45, 0), (0.0, 1)])
+def test_the_scale_in_base_2_must_be_a_number(scale, status):
+    d, a = T.model_desc(1, 8, 2, T.PAIR_NEOX, 1e4), 0x7000000000
+    assert T.lib().tria_prompt_attention(ctypes.byref(d), a, 1024, 128, a, 256, 128, a, 256, 128, 0, a, 1, scale, a, a, a,
+                                         256, None) == status
