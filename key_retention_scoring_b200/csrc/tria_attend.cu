@@ -26,8 +26,11 @@
 // A step is 64 keys, and each half has two buffers of S, so the product of the
 // next step is ready while the softmax of this one runs: with one 128-key
 // buffer the chain product, softmax, product set the pace (8448-token prompt,
-// 32 query and 8 KV heads: 597 us against 540 when both were built).  It takes
-// 520 us now, 1126 TFLOP/s.  What bounds it: the products alone take 449 us
+// 32 query and 8 KV heads: 597 us against 540 when both were built, single
+// launches).  In repetition, as the layers of a prefill follow one another, that
+// prompt takes 590 us (990 TFLOP/s, SM clock 1.67 GHz under the power cap), 16384
+// tokens of 64 query heads 4.25 ms (1035 TFLOP/s, 1.61 GHz; single launches at
+// 1.965 GHz 3.79 ms).  What bounds it, single launches: the products alone take 449 us
 // (Q K^T in steps of 64 keys reads more shared memory than the tensor core can
 // hide), the exponentials, conversions and maxima alone 433 us, and the two
 // share the warps' issue slots.

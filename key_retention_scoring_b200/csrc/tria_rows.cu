@@ -87,10 +87,11 @@ struct LayerPtrs {
 // above every destination already written, and within a chunk every read
 // comes before the barrier.  The path is checked by the threads while the
 // first chunk's rows are on their way (a source out of range is not read), and
-// one barrier serves both.  Up to 12 rows of 64 paged sequences x 32 layers x 8 KV
-// heads (102 MB) take 32 us, bound by the chain length -> path -> page -> row;
-// chunks of 32 rows and six blocks to an SM took 39 us in all against 43 before.
-// 4 rows of one sequence x 36 layers: 6 us.
+// one barrier serves both.  A position moves with its row, behind the row's page
+// check.  Up to 12 rows of 64 paged sequences x 32 layers x 8 KV heads (102 MB):
+// 34.7 us a call in all, 27 on the GPU, bound by the chain length -> path -> page
+// -> row; chunks of 32 rows and six blocks to an SM took 39 us in all against 43
+// with larger ones.  4 rows of one sequence x 36 layers: 6 us.
 // ---------------------------------------------------------------------------
 constexpr int kMoveU = 2;
 constexpr int kMoveRows = kMoveU * kMoveThreads / kPieces;  // rows of a chunk: 32
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kMoveThreads, 6) commit_kernel(const __grid_co
 // copies kForkRows slots of the K or V rows of one (group, layer), all KV
 // heads; slots whose block a destination shares are skipped for it.  Two private
 // copies of each of two sequences, 32 layers (2.02 GB): 330 us, 6.1 TB/s (HBM);
-// three children that share all but the last block (12 MB): 13 us (latency).
+// three children that share all but the last block (12 MB): 14 us (latency).
 // ---------------------------------------------------------------------------
 constexpr int kForkRows = 64;
 constexpr int kForkDst = 4;
