@@ -45,7 +45,7 @@ def expire(call, ws):
         flags = T.tria_read_device_status(ws)  # synchronises the stream
         # loads of a few us are waited for; a load looked for in the wrong phase of
         # its barrier would be waited for until the drain's own 2 s are over
-        assert time.monotonic() - t0 < 1.0
+        assert time.monotonic() - t0 < 1.9
     finally:
         T.tria_set_attention_wait_limit(0)
     assert flags in (0, WAIT_EXPIRED), flags
@@ -59,15 +59,18 @@ def expire(call, ws):
                          ids=["one", "short", "long", "many"])
 def test_prompt_wait_expires_and_the_next_call_is_right(lens):
     p = Prompt(32, 8, lens, seed=21, lead=3, tail=5)
+    expired = 0
     for _ in range(3):
         p.out.fill_(7.0)
         p.lse.fill_(7.0)
-        if not expire(p.run, p.ws):
-            # the limit is looked at when a sleep has run out, and the one short item's
-            # waits may all end within theirs: then the call is an ordinary one
-            assert lens == [5]
-            p.check(heads=[0, 31])
+        if expire(p.run, p.ws):
+            expired += 1
+        else:
+            # the limit is looked at when a sleep has run out, and all waits may have
+            # ended within theirs (one short item's do): then the call is an ordinary one
+            p.check(seqs=range(0, len(lens), 17), heads=[0, 31])
         p.untouched()
+    assert expired or lens == [5]
     p.run()
     p.check(seqs=range(0, len(lens), 17), heads=[0, 31])
     assert T.tria_read_device_status(p.ws) == 0
@@ -89,13 +92,15 @@ def test_tree_wait_expires_and_writes_no_rows_of_other_calls(block, n_draft):
         d.out, d.lse = out[16: 16 + n], lse[16: 16 + n]
         g = torch.Generator(device="cuda").manual_seed(24)
         for held in ("another call's records", "anything"):
+            expired = 0
             for _ in range(3):
                 far.run()
                 if held == "anything":
                     ws.copy_(torch.randint(0, 256, ws.shape, generator=g, device="cuda", dtype=torch.uint8))
-                assert expire(d.run, ws)
+                expired += expire(d.run, ws)
                 for x in (out, lse):
                     assert bool((x[:16] == 7.0).all()) and bool((x[16 + n:] == 7.0).all()), held
+            assert expired, held
         d.run()
         d.check(heads=[0, 13, 31])
         assert T.tria_read_device_status(ws) == 0
